@@ -344,6 +344,174 @@ ttt_status ttt_linear_backward_static(int B, int H, int T, int d, int mini_batch
                                       float* dV, float* deta, float* dW0, float* db0, float* dgamma,
                                       float* dbeta, ttt_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------- around the layer
+ * The operators of a block beside its sequence layer: the norm over the
+ * residual stream that opens it, the layer's projections from that norm's
+ * 8-bit output, and the selective state space scan with its short causal
+ * convolution, the neighbouring sequence layer that the pages compare
+ * TTT-Linear with (codewithpapers.app record, abstract).  The pages give no
+ * formulas for them; those below are the definitions.
+ *
+ * Token rows are [B][T][width].  dtype is the element type of every `const
+ * void*` / `void*` buffer; float* buffers are fp32.  Sums, statistics and states
+ * are fp32, and each output is rounded to its type once, to nearest.  Inputs
+ * with an `ld` are rows of `ld` elements (ld >= the width; the next sequence
+ * follows T * ld elements later), so a slice of a wider projection can be
+ * passed as it is; they need the alignment of their element only, every other
+ * pointer 16 bytes.  Rows on 16-byte boundaries are read 16 bytes at a time.
+ * lengths (or NULL) is a DEVICE array of B token counts for a padded batch:
+ * tokens at or past lengths[b] (taken into 0..T) are not read, leave the state
+ * as it is and have zeros as their outputs and gradients.
+ * Backward calls return gradients in the type of the input for token rows and
+ * in fp32 for parameters and states; sums over tokens, sequences or channels
+ * are taken in an order that the shape alone fixes.  They take a workspace as
+ * ttt_linear_backward does.  Other conventions as ttt_linear_forward: nothing
+ * is allocated or synchronised, arguments are checked before any launch.
+ */
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight
+ * over the d features of a token.  1 <= d <= 16384; B, T >= 1; eps > 0.
+ *   x, residual  [B][T][d]; residual may be NULL (h = x)
+ *   weight       [d] fp32
+ *   y            [B][T][d]
+ *   h            [B][T][d] or NULL: the residual stream, rounded (the norm is
+ *                taken of the unrounded sum).  y and h may each be the same
+ *                pointer as x or residual, for an update in place.
+ */
+ttt_status ttt_rmsnorm_forward(int B, int T, int d, ttt_dtype dtype, float eps, const void* x,
+                               const void* residual, const float* weight, void* y, void* h,
+                               ttt_stream_t stream);
+
+/* The same norm with its output in 8 bits (e4m3) and a scale a token, as
+ * ttt_prologue_q8_forward reads them:
+ *   scale = max(max |y| / 448, 2^-100),  q = e4m3(y / scale), to nearest
+ *   q      [B][T][d] bytes;  scale  [B][T]
+ */
+ttt_status ttt_rmsnorm_q8_forward(int B, int T, int d, ttt_dtype dtype, float eps, const void* x,
+                                  const void* residual, const float* weight, void* q, float* scale,
+                                  void* h, ttt_stream_t stream);
+
+/* Gradient of ttt_rmsnorm_forward.
+ *   h        [B][T][d]: the stream that was normed (the forward's h, or x)
+ *   dy       [B][T][d];  dh_in  [B][T][d] or NULL: the gradient that reaches h
+ *            past the norm
+ *   dh       [B][T][d]: the gradient of x and of residual alike; may be the
+ *            same pointer as dy or dh_in
+ *   dweight  [d] fp32
+ */
+size_t ttt_rmsnorm_backward_workspace_size(int B, int T, int d, ttt_dtype dtype);
+ttt_status ttt_rmsnorm_backward(int B, int T, int d, ttt_dtype dtype, float eps, const void* h,
+                                const float* weight, const void* dy, const void* dh_in, void* dh,
+                                float* dweight, void* workspace, size_t workspace_bytes,
+                                ttt_stream_t stream);
+
+/*
+ * ttt_prologue_forward with 8-bit operands (e4m3): x as ttt_rmsnorm_q8_forward
+ * writes it, weights laid out once with their features as rows and a scale
+ * each.  Q = (x . w) * scale_x * scale_w and so on; products are exact, sums in
+ * fp32, everything else as ttt_prologue_forward.
+ *   x        [B][T][d_model] e4m3;  scale_x  [B][T] fp32
+ *   theta_q, theta_k, theta_v  [H][d][d_model] e4m3;  scale_q, ...  [H][d] fp32
+ *   theta_lr [H][d_model] e4m3;  scale_lr [H] fp32;  b_lr [H] fp32
+ * Built for d = 64, d_model a multiple of 16, H a multiple of 4 up to 256
+ * (TTT_ERR_UNSUPPORTED otherwise); T >= 1.
+ */
+ttt_status ttt_prologue_q8_forward(int B, int T, int H, int d, int d_model, int pos0, float eta_base,
+                                   float rope_base, int rotary, const void* x, const float* scale_x,
+                                   const void* theta_q, const float* scale_q, const void* theta_k,
+                                   const float* scale_k, const void* theta_v, const float* scale_v,
+                                   const void* theta_lr, const float* scale_lr, const float* b_lr,
+                                   void* Q, void* K, void* V, float* eta, ttt_stream_t stream);
+
+/*
+ * Short causal depthwise convolution: per channel
+ *   y_t = act(bias + sum_{j < width} weight[j] x_{t - (width - 1) + j})
+ * with act the SiLU x / (1 + e^-x) (silu != 0) or the identity.  Rows before
+ * the first token are those of state0, or zero.  width 2, 3 or 4.
+ *   x        [B][T][C], rows of ld_x elements
+ *   weight   [C][width] fp32;  bias  [C] fp32 or NULL
+ *   state0   [B][width - 1][C] or NULL: the rows before x, oldest first
+ *   y        [B][T][C]
+ *   state_T  [B][width - 1][C] or NULL: the last rows up to each sequence's
+ *            end; may be the same pointer as state0
+ * T >= 0.
+ */
+ttt_status ttt_conv_forward(int B, int T, int C, int width, ttt_dtype dtype, int silu, long long ld_x,
+                            const void* x, const float* weight, const float* bias,
+                            const void* state0, const int* lengths, void* y, void* state_T,
+                            ttt_stream_t stream);
+
+/* The convolution continued by T >= 0 more tokens, one at a time in serving:
+ * state is read, then overwritten with the last width - 1 rows. */
+ttt_status ttt_conv_decode(int B, int T, int C, int width, ttt_dtype dtype, int silu, long long ld_x,
+                           const void* x, const float* weight, const float* bias, void* state, void* y,
+                           ttt_stream_t stream);
+
+/* Gradient of ttt_conv_forward.
+ *   dy       [B][T][C];  dstate_T  [B][width - 1][C] or NULL (zero)
+ *   dx       [B][T][C];  dweight  [C][width];  dbias  [C] or NULL
+ *   dstate0  [B][width - 1][C] or NULL
+ */
+size_t ttt_conv_backward_workspace_size(int B, int T, int C, int width);
+ttt_status ttt_conv_backward(int B, int T, int C, int width, ttt_dtype dtype, int silu, long long ld_x,
+                             const void* x, const float* weight, const float* bias,
+                             const void* state0, const int* lengths, const void* dy,
+                             const void* dstate_T, void* dx, float* dweight, float* dbias,
+                             void* dstate0, void* workspace, size_t workspace_bytes,
+                             ttt_stream_t stream);
+
+/*
+ * Selective state space scan: per channel c, with N states,
+ *   dt_t = softplus(dt[t] + dt_bias) (dt_softplus != 0) or dt[t] + dt_bias
+ *   h_t[n] = exp(dt_t A[n]) h_{t-1}[n] + dt_t u_t B_t[n]
+ *   y_t = (sum_n C_t[n] h_t[n] + D u_t) * silu(z_t)
+ * 1 <= N <= 64; A is taken as it is (negative for a state that decays).
+ *   u, dt    [B][T][C], rows of ld_u, ld_dt elements
+ *   dt_bias  [C] fp32 or NULL;  A  [C][N] fp32;  D  [C] fp32 or NULL
+ *   Bm, Cm   [B][T][N], rows of ld_b, ld_c elements, shared by all channels
+ *   z        [B][T][C], rows of ld_z elements, or NULL (no gate)
+ *   h0       [B][C][N] fp32 or NULL (zero)
+ *   y        [B][T][C];  h_T  [B][C][N] fp32: the state after each sequence's
+ *            last token; may be the same pointer as h0
+ * T >= 0.  workspace as in ttt_linear_backward; its size may be 0, and then
+ * it may be NULL.
+ */
+size_t ttt_ssm_forward_workspace_size(int B, int T, int C, int N);
+ttt_status ttt_ssm_forward(int B, int T, int C, int N, ttt_dtype dtype, int dt_softplus, long long ld_u,
+                           long long ld_dt, long long ld_b, long long ld_c, long long ld_z,
+                           const void* u, const void* dt, const float* dt_bias, const float* A,
+                           const void* Bm, const void* Cm, const float* D, const void* z,
+                           const float* h0, const int* lengths, void* y, float* h_T, void* workspace,
+                           size_t workspace_bytes, ttt_stream_t stream);
+
+/* The scan continued by T >= 0 more tokens, one at a time in serving: h is
+ * read, then overwritten with the state after the call's last token. */
+ttt_status ttt_ssm_decode(int B, int T, int C, int N, ttt_dtype dtype, int dt_softplus, long long ld_u,
+                          long long ld_dt, long long ld_b, long long ld_c, long long ld_z,
+                          const void* u, const void* dt, const float* dt_bias, const float* A,
+                          const void* Bm, const void* Cm, const float* D, const void* z, float* h,
+                          void* y, ttt_stream_t stream);
+
+/* Gradient of ttt_ssm_forward (from its inputs alone: the states are computed
+ * again).
+ *   dy       [B][T][C];  dh_T  [B][C][N] fp32 or NULL (zero)
+ *   du, ddt  [B][T][C] (ddt of the raw dt);  dz  [B][T][C], NULL where z is
+ *   dA       [C][N];  dB, dC  [B][T][N], all fp32
+ *   dD, ddt_bias  [C] fp32 or NULL;  dh0  [B][C][N] fp32 or NULL
+ */
+size_t ttt_ssm_backward_workspace_size(int B, int T, int C, int N);
+ttt_status ttt_ssm_backward(int B, int T, int C, int N, ttt_dtype dtype, int dt_softplus, long long ld_u,
+                            long long ld_dt, long long ld_b, long long ld_c, long long ld_z,
+                            const void* u, const void* dt, const float* dt_bias, const float* A,
+                            const void* Bm, const void* Cm, const float* D, const void* z,
+                            const float* h0, const int* lengths, const void* dy, const float* dh_T,
+                            void* du, void* ddt, float* dA, float* dB, float* dC, float* dD, void* dz,
+                            float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes,
+                            ttt_stream_t stream);
+
 /* Static string naming a status code; never NULL. */
 const char* ttt_status_string(ttt_status status);
 

@@ -455,3 +455,349 @@ def ttt_prologue_forward(x, theta_q, theta_k, theta_v, theta_lr, b_lr, *, pos0: 
                                   _ptr(Q), _ptr(K), _ptr(V), _ptr(eta), _stream_handle(dev, stream))
     _check(st)
     return Q, K, V, eta
+
+
+# ---------------------------------------------------------------- around the layer
+_L = ctypes.c_longlong
+_Z = ctypes.c_size_t
+lib.ttt_rmsnorm_forward.restype = _I
+lib.ttt_rmsnorm_forward.argtypes = [_I] * 4 + [_F] + [_P] * 6
+lib.ttt_rmsnorm_q8_forward.restype = _I
+lib.ttt_rmsnorm_q8_forward.argtypes = [_I] * 4 + [_F] + [_P] * 7
+lib.ttt_rmsnorm_backward_workspace_size.restype = _Z
+lib.ttt_rmsnorm_backward_workspace_size.argtypes = [_I] * 4
+lib.ttt_rmsnorm_backward.restype = _I
+lib.ttt_rmsnorm_backward.argtypes = [_I] * 4 + [_F] + [_P] * 7 + [_Z, _P]
+lib.ttt_prologue_q8_forward.restype = _I
+lib.ttt_prologue_q8_forward.argtypes = [_I] * 6 + [_F, _F, _I] + [_P] * 15 + [_P]
+lib.ttt_conv_forward.restype = _I
+lib.ttt_conv_forward.argtypes = [_I] * 6 + [_L] + [_P] * 7 + [_P]
+lib.ttt_conv_decode.restype = _I
+lib.ttt_conv_decode.argtypes = [_I] * 6 + [_L] + [_P] * 5 + [_P]
+lib.ttt_conv_backward_workspace_size.restype = _Z
+lib.ttt_conv_backward_workspace_size.argtypes = [_I] * 4
+lib.ttt_conv_backward.restype = _I
+lib.ttt_conv_backward.argtypes = [_I] * 6 + [_L] + [_P] * 12 + [_Z, _P]
+lib.ttt_ssm_forward_workspace_size.restype = _Z
+lib.ttt_ssm_forward_workspace_size.argtypes = [_I] * 4
+lib.ttt_ssm_forward.restype = _I
+lib.ttt_ssm_forward.argtypes = [_I] * 6 + [_L] * 5 + [_P] * 13 + [_Z, _P]
+lib.ttt_ssm_decode.restype = _I
+lib.ttt_ssm_decode.argtypes = [_I] * 6 + [_L] * 5 + [_P] * 10 + [_P]
+lib.ttt_ssm_backward_workspace_size.restype = _Z
+lib.ttt_ssm_backward_workspace_size.argtypes = [_I] * 4
+lib.ttt_ssm_backward.restype = _I
+lib.ttt_ssm_backward.argtypes = [_I] * 6 + [_L] * 5 + [_P] * 22 + [_Z, _P]
+
+
+class _Launch:
+    """Device and stream of one call: makes the tensors' device current and, where a stream is given, allocates
+    on it, so that the caching allocator knows which stream the call's buffers are used on."""
+
+    def __init__(self, dev: torch.device, stream):
+        self.device = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+        self.stream = None if stream is None else torch.cuda.stream(_launch_stream(dev, stream))
+        self.dev = dev
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _token_dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return TTT_BF16
+    if t.dtype == torch.float32:
+        return TTT_F32
+    raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
+
+
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> Optional[int]:
+    """Address of a contiguous CUDA tensor of this shape, type and device (None for None)."""
+    if t is None:
+        return None
+    if t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
+    """(address, row stride) of token rows [B, T, width], which may be a slice of wider rows."""
+    if t is None:
+        return None, 0
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    B, T, width = shape
+    sb, st, sw = t.stride()
+    ld = st if T > 1 else (sb if B > 1 else width)
+    if (sw != 1 and width > 1) or (B > 1 and T > 1 and sb != T * st) or (t.numel() and ld < width):
+        raise ValueError(f"{name} must have its elements side by side and its rows at one distance, "
+                         f"got strides {t.stride()}")
+    return t.data_ptr(), max(ld, width)
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, dev):
+    if given is None:
+        given = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif given.device != dev or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
+def _three(t: torch.Tensor, name: str):
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [B, T, width]")
+    return t.shape
+
+
+def ttt_rmsnorm_forward(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, stream=None):
+    """Root-mean-square norm of x + residual (see include/ttt.h).  Returns (y, h): h is the residual stream, None
+    where there is no residual and no h was given.  x, residual [B, T, d] bf16 or fp32, weight [d] fp32."""
+    B, T, d = _three(x, "x")
+    dev, dt = x.device, x.dtype
+    code = _token_dtype(x, "x")
+    px, pr = _dense(x, "x", (B, T, d), dt, dev), _dense(residual, "residual", (B, T, d), dt, dev)
+    pw = _dense(weight, "weight", (d,), torch.float32, dev)
+    with _Launch(dev, stream) as s:
+        y = torch.empty_like(x) if y is None else y
+        h = torch.empty_like(x) if h is None and residual is not None else h
+        _check(lib.ttt_rmsnorm_forward(B, T, d, code, eps, px, pr, pw, _dense(y, "y", (B, T, d), dt, dev),
+                                       _dense(h, "h", (B, T, d), dt, dev), s))
+    return y, h
+
+
+def ttt_rmsnorm_q8_forward(x, weight, residual=None, *, eps: float = 1e-6, q=None, scale=None, h=None, stream=None):
+    """The norm with its output in 8 bits (see include/ttt.h).  Returns (q, scale, h): q [B, T, d] float8_e4m3fn,
+    scale [B, T] fp32, h as in ttt_rmsnorm_forward."""
+    B, T, d = _three(x, "x")
+    dev, dt = x.device, x.dtype
+    code = _token_dtype(x, "x")
+    px, pr = _dense(x, "x", (B, T, d), dt, dev), _dense(residual, "residual", (B, T, d), dt, dev)
+    pw = _dense(weight, "weight", (d,), torch.float32, dev)
+    with _Launch(dev, stream) as s:
+        q = torch.empty((B, T, d), dtype=torch.float8_e4m3fn, device=dev) if q is None else q
+        scale = torch.empty((B, T), dtype=torch.float32, device=dev) if scale is None else scale
+        h = torch.empty_like(x) if h is None and residual is not None else h
+        _check(lib.ttt_rmsnorm_q8_forward(B, T, d, code, eps, px, pr, pw,
+                                          _dense(q, "q", (B, T, d), torch.float8_e4m3fn, dev),
+                                          _dense(scale, "scale", (B, T), torch.float32, dev),
+                                          _dense(h, "h", (B, T, d), dt, dev), s))
+    return q, scale, h
+
+
+def ttt_rmsnorm_backward(h, weight, dy, dh_in=None, *, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradient of the norm (see include/ttt.h).  Returns (dh, dweight): dh, in h's type, is the gradient of x and
+    of residual alike; dh_in is the gradient that reaches h past the norm."""
+    B, T, d = _three(h, "h")
+    dev, dt = h.device, h.dtype
+    code = _token_dtype(h, "h")
+    ph, pg = _dense(h, "h", (B, T, d), dt, dev), _dense(dy, "dy", (B, T, d), dt, dev)
+    pi = _dense(dh_in, "dh_in", (B, T, d), dt, dev)
+    pw = _dense(weight, "weight", (d,), torch.float32, dev)
+    with _Launch(dev, stream) as s:
+        dh, dw = torch.empty_like(h), torch.empty_like(weight)
+        workspace, pws, n = _workspace(workspace, lib.ttt_rmsnorm_backward_workspace_size(B, T, d, code), dev)
+        _check(lib.ttt_rmsnorm_backward(B, T, d, code, eps, ph, pw, pg, pi, dh.data_ptr(), dw.data_ptr(), pws, n, s))
+    return dh, dw
+
+
+def prologue_q8_weights(theta):
+    """Weights of ttt_prologue_q8_forward, laid out once: theta [H, d_model, d] (as ttt_prologue_forward takes it) or
+    theta_lr [H, d_model] to (e4m3 [H, d, d_model] or [H, d_model], fp32 scale [H, d] or [H])."""
+    rows = theta.float() if theta.dim() == 2 else theta.float().transpose(1, 2)
+    scale = (rows.abs().amax(-1) / 448.0).clamp_min(2.0 ** -100)
+    return (rows / scale[..., None]).to(torch.float8_e4m3fn).contiguous(), scale.contiguous()
+
+
+def ttt_prologue_q8_forward(x, scale_x, theta_q, scale_q, theta_k, scale_k, theta_v, scale_v, theta_lr, scale_lr, b_lr,
+                            *, pos0: int = 0, eta_base: float = 1.0, rope_base: float = 10000.0, rotary: bool = True,
+                            out=None, stream=None):
+    """The layer's prologue from 8-bit operands (see include/ttt.h): x and scale_x as ttt_rmsnorm_q8_forward returns
+    them, each weight and its scale as prologue_q8_weights does.  Returns Q, K, V [B, H, T, d] bf16 and eta [B, H, T]
+    fp32 (the tensors of `out` where given)."""
+    B, T, dm = _three(x, "x")
+    if theta_q.dim() != 3:
+        raise ValueError("theta_q must be [H, d, d_model]")
+    H, d = theta_q.shape[:2]
+    dev, f8, f32 = x.device, torch.float8_e4m3fn, torch.float32
+    ptrs = [_dense(x, "x", (B, T, dm), f8, dev), _dense(scale_x, "scale_x", (B, T), f32, dev)]
+    for name, w, sc in (("q", theta_q, scale_q), ("k", theta_k, scale_k), ("v", theta_v, scale_v)):
+        ptrs += [_dense(w, "theta_" + name, (H, d, dm), f8, dev), _dense(sc, "scale_" + name, (H, d), f32, dev)]
+    ptrs += [_dense(theta_lr, "theta_lr", (H, dm), f8, dev), _dense(scale_lr, "scale_lr", (H,), f32, dev),
+             _dense(b_lr, "b_lr", (H,), f32, dev)]
+    with _Launch(dev, stream) as s:
+        if out is None:
+            out = [torch.empty((B, H, T, d), dtype=torch.bfloat16, device=dev) for _ in range(3)]
+            out.append(torch.empty((B, H, T), dtype=f32, device=dev))
+        Q, K, V, eta = out
+        for name, o in (("Q", Q), ("K", K), ("V", V)):
+            ptrs.append(_dense(o, name, (B, H, T, d), torch.bfloat16, dev))
+        ptrs.append(_dense(eta, "eta", (B, H, T), f32, dev))
+        _check(lib.ttt_prologue_q8_forward(B, T, H, d, dm, int(pos0), float(eta_base), float(rope_base),
+                                           int(bool(rotary)), *ptrs, s))
+    return Q, K, V, eta
+
+
+def _silu_code(activation) -> int:
+    if activation not in ("silu", None):
+        raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
+    return int(activation == "silu")
+
+
+def _conv_args(x, weight, bias, state, lengths, state_name="state0"):
+    B, T, C = _three(x, "x")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C, width]")
+    W = weight.shape[1]
+    dev, dt = x.device, x.dtype
+    code = _token_dtype(x, "x")
+    px, ld = _rows(x, "x", (B, T, C), dt, dev)
+    pw = _dense(weight, "weight", (C, W), torch.float32, dev)
+    pb = _dense(bias, "bias", (C,), torch.float32, dev)
+    ps = _dense(state, state_name, (B, W - 1, C), dt, dev)
+    pl = _dense(lengths, "lengths", (B,), torch.int32, dev)
+    return (B, T, C, W, code), ld, (px, pw, pb, ps, pl)
+
+
+def ttt_conv_forward(x, weight, bias=None, state0=None, *, lengths=None, activation="silu", y=None, state_T=None,
+                     stream=None):
+    """Short causal depthwise convolution (see include/ttt.h).  x [B, T, C] bf16 or fp32 (a slice of wider rows will
+    do), weight [C, width] fp32, state0 [B, width - 1, C]: the rows before x.  Returns (y, state_T): the last
+    width - 1 rows of each sequence, to go on from."""
+    shape, ld, (px, pw, pb, ps, pl) = _conv_args(x, weight, bias, state0, lengths)
+    B, T, C, W, _ = shape
+    dev, dt = x.device, x.dtype
+    with _Launch(dev, stream) as s:
+        y = torch.empty((B, T, C), dtype=dt, device=dev) if y is None else y
+        state_T = torch.empty((B, W - 1, C), dtype=dt, device=dev) if state_T is None else state_T
+        _check(lib.ttt_conv_forward(*shape, _silu_code(activation), ld, px, pw, pb, ps, pl,
+                                    _dense(y, "y", (B, T, C), dt, dev),
+                                    _dense(state_T, "state_T", (B, W - 1, C), dt, dev), s))
+    return y, state_T
+
+
+def ttt_conv_decode(x, weight, bias, state, *, activation="silu", y=None, stream=None):
+    """The convolution continued by x's tokens (see include/ttt.h); state [B, width - 1, C] is updated in place.
+    Returns y."""
+    if state is None:
+        raise ValueError("state must be a contiguous CUDA tensor")
+    shape, ld, (px, pw, pb, ps, _) = _conv_args(x, weight, bias, state, None, "state")
+    B, T, C, W, _ = shape
+    dev, dt = x.device, x.dtype
+    with _Launch(dev, stream) as s:
+        y = torch.empty((B, T, C), dtype=dt, device=dev) if y is None else y
+        _check(lib.ttt_conv_decode(*shape, _silu_code(activation), ld, px, pw, pb, ps,
+                                   _dense(y, "y", (B, T, C), dt, dev), s))
+    return y
+
+
+def ttt_conv_backward(x, weight, bias, dy, state0=None, dstate_T=None, *, lengths=None, activation="silu",
+                      workspace=None, stream=None):
+    """Gradient of the convolution (see include/ttt.h).  Returns (dx, dweight, dbias, dstate0); dbias is None where
+    bias is, dstate0 where state0 is."""
+    shape, ld, (px, pw, pb, ps, pl) = _conv_args(x, weight, bias, state0, lengths)
+    B, T, C, W, code = shape
+    dev, dt = x.device, x.dtype
+    pg = _dense(dy, "dy", (B, T, C), dt, dev)
+    pt = _dense(dstate_T, "dstate_T", (B, W - 1, C), dt, dev)
+    with _Launch(dev, stream) as s:
+        dx, dw = torch.empty((B, T, C), dtype=dt, device=dev), torch.empty_like(weight)
+        db = None if bias is None else torch.empty_like(bias)
+        d0 = None if state0 is None else torch.empty_like(state0)
+        workspace, pws, n = _workspace(workspace, lib.ttt_conv_backward_workspace_size(B, T, C, W), dev)
+        _check(lib.ttt_conv_backward(*shape, _silu_code(activation), ld, px, pw, pb, ps, pl, pg, pt, dx.data_ptr(),
+                                     dw.data_ptr(), _ptr(db), _ptr(d0), pws, n, s))
+    return dx, dw, db, d0
+
+
+def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, h_name="h0"):
+    B, T, C = _three(u, "u")
+    if A.dim() != 2:
+        raise ValueError("A must be [C, N]")
+    N = A.shape[1]
+    dev, ty, f32 = u.device, u.dtype, torch.float32
+    code = _token_dtype(u, "u")
+    pu, lu = _rows(u, "u", (B, T, C), ty, dev)
+    pd, ld = _rows(dt, "dt", (B, T, C), ty, dev)
+    pB, lB = _rows(Bm, "Bm", (B, T, N), ty, dev)
+    pC, lC = _rows(Cm, "Cm", (B, T, N), ty, dev)
+    pz, lz = _rows(z, "z", (B, T, C), ty, dev)
+    pbias = _dense(dt_bias, "dt_bias", (C,), f32, dev)
+    pA, pD = _dense(A, "A", (C, N), f32, dev), _dense(D, "D", (C,), f32, dev)
+    ph = _dense(h0, h_name, (B, C, N), f32, dev)
+    pl = _dense(lengths, "lengths", (B,), torch.int32, dev)
+    return (B, T, C, N, code), (lu, ld, lB, lC, lz), (pu, pd, pbias, pA, pB, pC, pD, pz, ph, pl)
+
+
+def ttt_ssm_forward(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, lengths=None, dt_softplus: bool = True,
+                    y=None, h_T=None, workspace=None, stream=None):
+    """Selective state space scan (see include/ttt.h).  u, dt, z [B, T, C] and Bm, Cm [B, T, N], bf16 or fp32 (slices
+    of wider rows will do); A [C, N], D, dt_bias [C], h0 [B, C, N] fp32.  Returns (y, h_T)."""
+    shape, lds, ptrs = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths)
+    B, T, C, N, _ = shape
+    dev = u.device
+    with _Launch(dev, stream) as s:
+        y = torch.empty((B, T, C), dtype=u.dtype, device=dev) if y is None else y
+        h_T = torch.empty((B, C, N), dtype=torch.float32, device=dev) if h_T is None else h_T
+        need = lib.ttt_ssm_forward_workspace_size(B, T, C, N)
+        pws, n = None, 0
+        if need or workspace is not None:
+            workspace, pws, n = _workspace(workspace, need, dev)
+        _check(lib.ttt_ssm_forward(*shape, int(bool(dt_softplus)), *lds, *ptrs, _dense(y, "y", (B, T, C), u.dtype, dev),
+                                   _dense(h_T, "h_T", (B, C, N), torch.float32, dev), pws, n, s))
+    return y, h_T
+
+
+def ttt_ssm_decode(u, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, *, dt_softplus: bool = True, y=None, stream=None):
+    """The scan continued by u's tokens (see include/ttt.h); h [B, C, N] is updated in place.  Returns y."""
+    if h is None:
+        raise ValueError("h must be a contiguous CUDA tensor")
+    shape, lds, ptrs = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, h, None, "h")
+    B, T, C, N, _ = shape
+    dev = u.device
+    with _Launch(dev, stream) as s:
+        y = torch.empty((B, T, C), dtype=u.dtype, device=dev) if y is None else y
+        _check(lib.ttt_ssm_decode(*shape, int(bool(dt_softplus)), *lds, *ptrs[:-1],
+                                  _dense(y, "y", (B, T, C), u.dtype, dev), s))
+    return y
+
+
+def ttt_ssm_backward(u, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, h0=None, dh_T=None, *, lengths=None,
+                     dt_softplus: bool = True, workspace=None, stream=None):
+    """Gradient of the scan (see include/ttt.h), from its inputs and dy [B, T, C], dh_T [B, C, N].  Returns (du, ddt,
+    dA, dB, dC, dD, dz, ddt_bias, dh0): token rows in u's type, the rest fp32; None for an input that is None."""
+    shape, lds, ptrs = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths)
+    B, T, C, N, _ = shape
+    dev, f32 = u.device, torch.float32
+    pg = _dense(dy, "dy", (B, T, C), u.dtype, dev)
+    pt = _dense(dh_T, "dh_T", (B, C, N), f32, dev)
+    with _Launch(dev, stream) as s:
+        du, ddt = (torch.empty((B, T, C), dtype=u.dtype, device=dev) for _ in range(2))
+        dz = None if z is None else torch.empty((B, T, C), dtype=u.dtype, device=dev)
+        dA = torch.empty_like(A)
+        dB, dC = (torch.empty((B, T, N), dtype=f32, device=dev) for _ in range(2))
+        dD = None if D is None else torch.empty_like(D)
+        dbias = None if dt_bias is None else torch.empty_like(dt_bias)
+        dh0 = None if h0 is None else torch.empty_like(h0)
+        workspace, pws, n = _workspace(workspace, lib.ttt_ssm_backward_workspace_size(B, T, C, N), dev)
+        _check(lib.ttt_ssm_backward(*shape, int(bool(dt_softplus)), *lds, *ptrs, pg, pt, du.data_ptr(), ddt.data_ptr(),
+                                    dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), _ptr(dD), _ptr(dz), _ptr(dbias),
+                                    _ptr(dh0), pws, n, s))
+    return du, ddt, dA, dB, dC, dD, dz, dbias, dh0

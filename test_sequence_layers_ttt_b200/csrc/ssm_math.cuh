@@ -1,0 +1,84 @@
+// Arithmetic of the selective scan shared by its forward, decode and backward kernels.
+//
+// The decay a = e^(dt A) = 2^x with x = dt A log2(e).  Where a is close to 1 the state remembers about
+// 1 / |x| tokens, so an error of a that does not average out grows by that factor; the special-function
+// unit's 2^x is off by up to 2^-22 and, between -1/16 and 0, by 2.5e-8 low on average (measured over
+// 2^20 points an octave).  So for |x| < 1/16 the decay is 1 + x q(x) with q the quadratic that fits
+// (2^x - 1) / x on [-1/16, 0] to 1.3e-7 (Remez exchange; within 1e-5 up to +1/16, for a state that
+// grows): 1 - a is then right to 1.3e-7 whatever its size, and only the last rounding, which is to
+// nearest, is left.  Beyond it the unit's result stands: its error counts at most 16 times there.
+// The cost is three of the pipe's fused multiply-adds a state beside one special-function result
+// (16 a clock an SM), which stays the bound.
+#pragma once
+
+#include "common.cuh"
+
+namespace ttt {
+namespace ssm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSmall = 0.0625f;
+constexpr float kQ0 = 0x1.62e42ep-1f, kQ1 = 0x1.ebf0e6p-3f, kQ2 = 0x1.bf5dd8p-5f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float decay(float x) {
+    const float q = fmaf(fmaf(kQ2, x, kQ1), x, kQ0);
+    const float near_one = fmaf(q, x, 1.f);
+    return fabsf(x) < kSmall ? near_one : ex2(x);
+}
+
+// softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1]: log(1 + e) = 2 atanh(s), s = e / (2 + e) in
+// (0, 1/3], by an even polynomial that fits 2 atanh(s) / s to 8e-9; right to a few 1e-7 of the result at any x.
+__device__ __forceinline__ float softplus(float x) {
+    const float e = ex2(-kLog2e * fabsf(x));
+    const float s = __fdividef(e, 2.f + e), w = s * s;
+    float p = 0x1.208bd0p-2f;
+    p = fmaf(p, w, 0x1.1e510ap-2f);
+    p = fmaf(p, w, 0x1.99dae6p-2f);
+    p = fmaf(p, w, 0x1.5554e0p-1f);
+    p = fmaf(p, w, 2.f);
+    return fmaf(s, p, fmaxf(x, 0.f));
+}
+
+// Two floats in one 64-bit register pair, for the packed fp32 instructions of sm_100.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 decay2(f2 x) {
+    const f2 q = fma2(fma2(pack2(kQ2, kQ2), x, pack2(kQ1, kQ1)), x, pack2(kQ0, kQ0));
+    const f2 near_one = fma2(q, x, pack2(1.f, 1.f));
+    float x0, x1, n0, n1;
+    unpack2(x, x0, x1);
+    unpack2(near_one, n0, n1);
+    return pack2(fabsf(x0) < kSmall ? n0 : ex2(x0), fabsf(x1) < kSmall ? n1 : ex2(x1));
+}
+
+__device__ __forceinline__ int length_of(const int* lengths, int b, int T) {
+    if (!lengths) return T;
+    const int n = lengths[b];
+    return n < 0 ? 0 : (n > T ? T : n);
+}
+
+}  // namespace ssm
+}  // namespace ttt

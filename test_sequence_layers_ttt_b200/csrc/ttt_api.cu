@@ -6,6 +6,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "api_util.h"
 #include "ttt_internal.h"
 
 namespace ttt {
@@ -17,70 +18,15 @@ cudaError_t launch_mlp_decode(const MlpArgs& a, cudaStream_t stream);
 
 namespace {
 
+using ttt::aligned16;
+using ttt::check_aliasing;
+using ttt::finish;
 using ttt::LinearArgs;
 using ttt::MlpArgs;
-
-struct Span {
-    const void* p;
-    size_t bytes;
-};
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlap(Span a, Span b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool check_env() {
-    static const bool on = [] {
-        const char* v = std::getenv("TTT_CHECK");
-        return v && v[0] && std::strcmp(v, "0") != 0;
-    }();
-    // the fault-injection hook makes a launch abandon its waits: report that as a status
-    return on || ttt::drop_chunk_hook() >= 0;
-}
-
-// In check mode the device error words are cleared before the launch, so the
-// status a checked call returns reflects that call alone (calls overlapping on
-// several streams still share the words).
-bool prepare() {
-    if (!check_env()) return true;
-    unsigned int stale = 0;
-    return ttt::read_and_clear_device_error(&stale) == cudaSuccess &&
-           ttt::read_and_clear_mlp_error(&stale) == cudaSuccess &&
-           ttt::read_and_clear_umma_error(&stale) == cudaSuccess &&
-           ttt::read_and_clear_prologue_error(&stale) == cudaSuccess;
-}
+using ttt::prepare;
+using ttt::Span;
 
 bool valid_mini_batch(int mb) { return mb >= 1 && (mb % 16 == 0 || mb == 1 || mb == 2 || mb == 4 || mb == 8); }
-
-// Outputs must not overlap any other buffer, except that an output state
-// buffer may be exactly its initial-state buffer (in-place update).
-ttt_status check_aliasing(const Span* outs, int n_out, const Span* ins, const int* same_as, int n_in) {
-    for (int o = 0; o < n_out; o++) {
-        for (int i = 0; i < n_in; i++) {
-            if (same_as[o] == i && outs[o].p == ins[i].p) continue;
-            if (overlap(outs[o], ins[i])) return TTT_ERR_ALIAS;
-        }
-        for (int o2 = o + 1; o2 < n_out; o2++)
-            if (overlap(outs[o], outs[o2])) return TTT_ERR_ALIAS;
-    }
-    return TTT_OK;
-}
-
-ttt_status finish(cudaError_t launch, cudaStream_t stream) {
-    if (launch != cudaSuccess) return TTT_ERR_CUDA;
-    if (!check_env()) return TTT_OK;
-    if (cudaStreamSynchronize(stream) != cudaSuccess) return TTT_ERR_CUDA;
-    unsigned int flag = 0, mlp_flag = 0, umma_flag = 0, pro_flag = 0;
-    if (ttt::read_and_clear_device_error(&flag) != cudaSuccess) return TTT_ERR_CUDA;
-    if (ttt::read_and_clear_mlp_error(&mlp_flag) != cudaSuccess) return TTT_ERR_CUDA;
-    if (ttt::read_and_clear_umma_error(&umma_flag) != cudaSuccess) return TTT_ERR_CUDA;
-    if (ttt::read_and_clear_prologue_error(&pro_flag) != cudaSuccess) return TTT_ERR_CUDA;
-    return (flag | mlp_flag | umma_flag | pro_flag) ? TTT_ERR_TIMEOUT : TTT_OK;
-}
 
 ttt_status validate_linear(const LinearArgs& a) {
     if (a.B < 1 || a.H < 1 || a.T < 0 || (long long)a.B * a.H > INT_MAX) return TTT_ERR_SHAPE;

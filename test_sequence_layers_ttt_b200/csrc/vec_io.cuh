@@ -1,0 +1,88 @@
+// Loads and stores of V neighbouring elements of a token row as floats: 16 bytes at once where V
+// fills them (the caller has checked the alignment), one element for V = 1.  Rounding to bf16 is to
+// nearest, once, at the store.
+#pragma once
+
+#include "common.cuh"
+
+namespace ttt {
+
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+    static constexpr int kVec = 8;  // elements in 16 bytes
+};
+template <> struct Elem<float> {
+    static constexpr int kVec = 4;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int V>
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[V]) {
+    static_assert(V == 1 || V == 4 || V == 8, "widths in use");
+    if constexpr (V == 8) {
+        const uint4 r = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else if constexpr (V == 4) {
+        const uint2 r = *reinterpret_cast<const uint2*>(p);
+        v[0] = __uint_as_float(r.x << 16);
+        v[1] = __uint_as_float(r.x & 0xffff0000u);
+        v[2] = __uint_as_float(r.y << 16);
+        v[3] = __uint_as_float(r.y & 0xffff0000u);
+    } else {
+        v[0] = __bfloat162float(*p);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_vec(const float* p, float (&v)[V]) {
+    static_assert(V == 1 || V == 4 || V == 8, "widths in use");
+    if constexpr (V == 1) {
+        v[0] = *p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; i++) {
+            const float4 r = reinterpret_cast<const float4*>(p)[i];
+            v[4 * i] = r.x;
+            v[4 * i + 1] = r.y;
+            v[4 * i + 2] = r.z;
+            v[4 * i + 3] = r.w;
+        }
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[V]) {
+    if constexpr (V == 8) {
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else if constexpr (V == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else {
+        *p = __float2bfloat16_rn(v[0]);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *p = v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; i++)
+            reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+}
+
+// logistic function; 1 / (1 + e^-x) with e^-x = 0 or infinity at the ends gives 1 or 0
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+}  // namespace ttt

@@ -1,0 +1,273 @@
+"""The selective scan kernels against the float64 oracle (oracle/block.py), within the float32 bound that the oracle
+carries through the recursion and half a step of the output's type.  Everything that must not be read is NaN."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import block_cases as bc
+from oracle import block as ob
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+GRADS = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")
+
+
+@pytest.fixture(scope="module")
+def ttt(cuda_device):
+    from test_sequence_layers_ttt_b200 import _binding
+    return _binding
+
+
+def forward(ttt, i, **kw):
+    return ttt.ttt_ssm_forward(i["u"], i["dt"], i["A"], i["Bm"], i["Cm"], i.get("D"), i.get("z"), i.get("dt_bias"),
+                               i.get("h0"), **kw)
+
+
+def backward(ttt, i, dy, dh=None, **kw):
+    out = ttt.ttt_ssm_backward(i["u"], i["dt"], i["A"], i["Bm"], i["Cm"], dy, i.get("D"), i.get("z"), i.get("dt_bias"),
+                               i.get("h0"), dh, **kw)
+    return dict(zip(GRADS, out))
+
+
+def check_forward(got, i, **kw):
+    (yo, ye), (ho, he) = ob.ssm(**i, **kw)
+    bc.close("y", got[0], yo, ye)
+    bc.close("h_T", got[1], ho, he)
+
+
+def check_backward(got, i, dy, dh, **kw):
+    want = ob.ssm_backward(i["u"], i["dt"], i["A"], i["Bm"], i["Cm"], dy, i.get("D"), i.get("z"), i.get("dt_bias"),
+                           i.get("h0"), dh, **kw)
+    for k, v in got.items():
+        if v is not None:
+            bc.close(k, v, *want[k])
+
+
+# states: 1, odd ones, every power of two and one past it; tokens: one, tile borders and their neighbours
+SIZES = [(1, 1, 1, 1), (2, 3, 5, 1), (1, 16, 32, 4), (2, 17, 33, 5), (1, 15, 64, 8), (3, 33, 40, 9), (2, 64, 96, 16),
+         (1, 100, 31, 16), (1, 65, 130, 17), (2, 48, 20, 32), (1, 50, 36, 33), (1, 31, 70, 64), (2, 200, 12, 16)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,N", SIZES)
+def test_forward(ttt, B, T, C, N, kind):
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=T)
+    check_forward(forward(ttt, bc.cuda(i)), i)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("missing", [("D",), ("z",), ("dt_bias",), ("h0",), ("D", "z", "h0")])
+def test_forward_without_its_options(ttt, missing, kind):
+    i = bc.ssm_inputs(2, 21, 36, 16, kind, seed=1)
+    if "dt_bias" in missing:
+        i["dt"] = (i["dt"].float() - 3.0).to(i["dt"].dtype)
+    i = {k: v for k, v in i.items() if k not in missing}
+    check_forward(forward(ttt, bc.cuda(i)), i)
+
+
+def test_forward_without_softplus_and_with_growing_states(ttt):
+    i = bc.ssm_inputs(2, 40, 33, 8, "f32", seed=2, softplus=False)
+    check_forward(forward(ttt, bc.cuda(i), dt_softplus=False), i, softplus=False)
+    i["A"] = -0.5 * i["A"]  # states that grow, over decays near 1 and far from it
+    check_forward(forward(ttt, bc.cuda(i), dt_softplus=False), i, softplus=False)
+
+
+def test_large_and_small_steps(ttt):
+    """Raw steps from -100 (nothing passes, the state stays) to 100 (the state is forgotten at once)."""
+    i = bc.ssm_inputs(1, 24, 32, 16, "f32", seed=3)
+    i["dt"] = torch.linspace(-100, 100, 24)[None, :, None].expand(1, 24, 32).contiguous()
+    check_forward(forward(ttt, bc.cuda(i)), i)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,N", [(4, 70, 40, 16), (5, 16, 33, 16), (3, 100, 64, 5), (6, 2, 32, 64)])
+def test_padded_batch(ttt, B, T, C, N, kind):
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=4)
+    n = bc.lengths_for(B, T, torch.Generator().manual_seed(5))
+    for b in range(B):
+        for k in ("u", "dt", "Bm", "Cm", "z"):
+            i[k][b, n[b]:] = NAN
+    y, h = forward(ttt, bc.cuda(i), lengths=n.cuda())
+    check_forward((y, h), i, lengths=n)
+    for b in range(B):
+        assert not y[b, n[b]:].any()
+    assert torch.equal(h[B // 2].cpu(), i["h0"][B // 2])  # the empty sequence's state
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("before,after", [(0, 64), (16, 16), (3, 2)])
+def test_slices_of_wider_rows(ttt, before, after, kind):
+    i = bc.ssm_inputs(2, 37, 40, 16, kind, seed=6)
+    want = forward(ttt, bc.cuda(i))
+    c = bc.cuda(i)
+    for k in ("u", "dt", "Bm", "Cm", "z"):
+        wide, at = bc.slice_of(i[k], before, after)
+        c[k] = wide.cuda()[at]
+    got = forward(ttt, c)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.Generator().manual_seed(0)
+    dy = bc.normal(g, 2, 37, 40).to(i["u"].dtype)
+    check_backward(backward(ttt, c, dy.cuda()), i, dy, None)
+
+
+def test_the_state_goes_in_place(ttt):
+    i = bc.cuda(bc.ssm_inputs(3, 300, 64, 16, "bf16", seed=7))
+    y, h = forward(ttt, i)
+    kept = i["h0"].clone()
+    y2, h2 = forward(ttt, i, h_T=i["h0"])
+    assert h2 is i["h0"] and torch.equal(h2, h) and torch.equal(y2, y) and not torch.equal(kept, h2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 6, 16, 40])
+def test_decode(ttt, N, kind):
+    """Tokens in pieces of 1, 2 and 7 in place, against the oracle over the whole stream."""
+    i = bc.ssm_inputs(3, 13, 37, N, kind, seed=8)
+    c = bc.cuda(i)
+    h, t, ys = c["h0"].clone(), 0, []
+    for k in (1, 2, 1, 7, 1, 1):
+        p = {n: c[n][:, t:t + k].contiguous() for n in ("u", "dt", "Bm", "Cm", "z")}
+        ys.append(ttt.ttt_ssm_decode(p["u"], p["dt"], c["A"], p["Bm"], p["Cm"], h, c["D"], p["z"], c["dt_bias"]))
+        t += k
+    assert t == 13
+    check_forward((torch.cat(ys, 1), h), i)
+
+
+def test_decode_continues_a_prompt(ttt):
+    i = bc.ssm_inputs(2, 80, 64, 16, "f32", seed=9)
+    c = bc.cuda(i)
+    part = {n: (v[:, :70].contiguous() if n in ("u", "dt", "Bm", "Cm", "z") else v) for n, v in c.items()}
+    y, h = forward(ttt, part)
+    ys = [y]
+    for t in range(70, 80):
+        p = {n: c[n][:, t:t + 1].contiguous() for n in ("u", "dt", "Bm", "Cm", "z")}
+        ys.append(ttt.ttt_ssm_decode(p["u"], p["dt"], c["A"], p["Bm"], p["Cm"], h, c["D"], p["z"], c["dt_bias"]))
+    check_forward((torch.cat(ys, 1), h), i)
+
+
+def test_no_tokens(ttt):
+    i = bc.cuda(bc.ssm_inputs(2, 4, 40, 16, "bf16", seed=10))
+    e = {n: (v[:, :0].contiguous() if n in ("u", "dt", "Bm", "Cm", "z") else v) for n, v in i.items()}
+    y, h = forward(ttt, e)
+    assert y.numel() == 0 and torch.equal(h, i["h0"])
+    y, h = forward(ttt, {k: v for k, v in e.items() if k != "h0"})
+    assert not h.any()
+    out = backward(ttt, e, e["u"], i["h0"])
+    assert torch.equal(out["dh0"], i["h0"]) and not out["dA"].any() and not out["dD"].any() and not out["ddt_bias"].any()
+    h = i["h0"].clone()
+    ttt.ttt_ssm_decode(e["u"], e["dt"], e["A"], e["Bm"], e["Cm"], h)
+    assert torch.equal(h, i["h0"])
+
+
+@pytest.mark.parametrize("B,T,C,N", [(1, 4000, 32, 16), (2, 1111, 70, 16), (1, 1025, 8, 3), (1, 2048, 20, 64)])
+def test_few_rows_long(ttt, B, T, C, N):
+    """Few channels and a long sequence: the sequence is worked on in pieces."""
+    i = bc.ssm_inputs(B, T, C, N, "f32", seed=11)
+    check_forward(forward(ttt, bc.cuda(i)), i)
+
+
+def test_few_rows_long_padded(ttt):
+    B, T = 3, 1500
+    i = bc.ssm_inputs(B, T, 40, 16, "bf16", seed=12)
+    n = torch.tensor([T, 0, 777], dtype=torch.int32)
+    for b in range(B):
+        for k in ("u", "dt", "Bm", "Cm", "z"):
+            i[k][b, n[b]:] = NAN
+    check_forward(forward(ttt, bc.cuda(i), lengths=n.cuda()), i, lengths=n)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,N", SIZES)
+def test_backward(ttt, B, T, C, N, kind):
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=100 + T)
+    g = torch.Generator().manual_seed(T)
+    dy, dh = bc.normal(g, B, T, C).to(i["u"].dtype), bc.normal(g, B, C, N)
+    check_backward(backward(ttt, bc.cuda(i), dy.cuda(), dh.cuda()), i, dy, dh)
+
+
+@pytest.mark.parametrize("missing", [("D",), ("z",), ("dt_bias",), ("h0",), ("D", "z", "h0")])
+def test_backward_without_its_options(ttt, missing):
+    i = bc.ssm_inputs(2, 21, 36, 16, "f32", seed=13)
+    if "dt_bias" in missing:
+        i["dt"] -= 3.0
+    i = {k: v for k, v in i.items() if k not in missing}
+    dy = bc.normal(torch.Generator().manual_seed(1), 2, 21, 36)
+    out = backward(ttt, bc.cuda(i), dy.cuda())
+    check_backward(out, i, dy, None)
+    for leaf, grad in (("D", "dD"), ("z", "dz"), ("dt_bias", "ddt_bias"), ("h0", "dh0")):
+        assert (out[grad] is None) == (leaf in missing)
+
+
+def test_backward_without_softplus(ttt):
+    i = bc.ssm_inputs(2, 40, 33, 8, "f32", seed=14, softplus=False)
+    dy = bc.normal(torch.Generator().manual_seed(1), 2, 40, 33)
+    check_backward(backward(ttt, bc.cuda(i), dy.cuda(), dt_softplus=False), i, dy, None, softplus=False)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,N", [(4, 70, 40, 16), (5, 16, 33, 16), (3, 100, 64, 5), (6, 2, 32, 64)])
+def test_backward_of_a_padded_batch(ttt, B, T, C, N, kind):
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=15)
+    g = torch.Generator().manual_seed(5)
+    n = bc.lengths_for(B, T, g)
+    dy, dh = bc.normal(g, B, T, C).to(i["u"].dtype), bc.normal(g, B, C, N)
+    for b in range(B):
+        dy[b, n[b]:] = NAN
+        for k in ("u", "dt", "Bm", "Cm", "z"):
+            i[k][b, n[b]:] = NAN
+    out = backward(ttt, bc.cuda(i), dy.cuda(), dh.cuda(), lengths=n.cuda())
+    check_backward(out, i, dy, dh, lengths=n)
+    for b in range(B):
+        for k in ("du", "ddt", "dz", "dB", "dC"):
+            assert not out[k][b, n[b]:].any(), k
+
+
+@pytest.mark.parametrize("B,T,C,N", [(1, 1500, 40, 16), (1, 700, 20, 33)])
+def test_backward_few_rows_long(ttt, B, T, C, N):
+    i = bc.ssm_inputs(B, T, C, N, "f32", seed=16)
+    g = torch.Generator().manual_seed(6)
+    dy, dh = bc.normal(g, B, T, C), bc.normal(g, B, C, N)
+    check_backward(backward(ttt, bc.cuda(i), dy.cuda(), dh.cuda()), i, dy, dh)
+
+
+def test_backward_twice_is_the_same(ttt):
+    i = bc.cuda(bc.ssm_inputs(3, 300, 200, 16, "bf16", seed=17))
+    one, two = backward(ttt, i, i["u"]), backward(ttt, i, i["u"])
+    assert all(torch.equal(one[k], two[k]) for k in GRADS)
+
+
+def test_offsets_past_32_bits(ttt):
+    """2.2e9 elements: the last sequence equals itself alone."""
+    B, T, C, N = 66, 4096, 8192, 2
+    u = torch.zeros(B, T, C, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    u[-1] = torch.randn(T, C, generator=g, device="cuda").bfloat16()
+    dt = torch.full_like(u, -2.0)
+    Bm = torch.randn(B, T, N, generator=g, device="cuda").bfloat16()
+    A = -torch.ones(C, N, device="cuda")
+    y, h = ttt.ttt_ssm_forward(u, dt, A, Bm, Bm)
+    last = {"u": u[-1:].contiguous(), "dt": dt[-1:].contiguous(), "A": A, "Bm": Bm[-1:].contiguous(), "Cm": Bm[-1:].contiguous()}
+    del u, dt
+    ya, ha = forward(ttt, last)
+    assert torch.allclose(y[-1:].float(), ya.float(), rtol=2 ** -7, atol=1e-5) and torch.allclose(h[-1:], ha, rtol=1e-4, atol=1e-6)
+
+
+def test_refusals_of_the_binding(ttt):
+    i = bc.cuda(bc.ssm_inputs(2, 6, 16, 4, "f32", seed=18))
+    with pytest.raises(TypeError, match="Bm must be"):
+        forward(ttt, {**i, "Bm": i["Bm"].bfloat16()})
+    with pytest.raises(ValueError, match="Cm must be"):
+        forward(ttt, {**i, "Cm": i["Cm"][:, :, :3]})
+    with pytest.raises(ValueError, match="A must be"):
+        forward(ttt, {**i, "A": i["A"][:8]})
+    with pytest.raises(ValueError, match="rows at one distance"):
+        forward(ttt, {**i, "u": torch.cat((i["u"], i["u"]), 1)[:, :6]})
+    with pytest.raises(ValueError, match="dy must be"):
+        backward(ttt, i, i["u"][:, :5])
+    with pytest.raises(ttt.TTTError) as e:
+        forward(ttt, i, y=i["z"])
+    assert e.value.status == 5
+    with pytest.raises(ttt.TTTError) as e:
+        backward(ttt, i, i["u"], workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 9
