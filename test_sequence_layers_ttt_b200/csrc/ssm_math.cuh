@@ -71,7 +71,9 @@ __device__ __forceinline__ f2 decay2(f2 x) {
     float x0, x1, n0, n1;
     unpack2(x, x0, x1);
     unpack2(near_one, n0, n1);
-    return pack2(fabsf(x0) < kSmall ? n0 : ex2(x0), fabsf(x1) < kSmall ? n1 : ex2(x1));
+    if (!(fabsf(x0) < kSmall)) n0 = ex2(x0);
+    if (!(fabsf(x1) < kSmall)) n1 = ex2(x1);
+    return pack2(n0, n1);
 }
 
 __device__ __forceinline__ int length_of(const int* lengths, int b, int T) {

@@ -98,12 +98,16 @@ __global__ void __launch_bounds__(1024) ttt_rmsnorm_kernel(const NormParams p) {
     }
     acc = reduce_row<true>(acc, s);
     const float r = rsqrtf(acc.x / (float)p.d + p.eps);
-    float scale = 1.f, inv = 1.f;
+    float inv = 1.f;  // y / scale = (h w) inv
     if (kQ8) {
-        scale = acc.y * r * (1.f / kE4m3Max);
-        if (r != r) scale = r;
-        else if (!(scale >= kScaleMin)) scale = kScaleMin;
-        inv = 1.f / scale;  // at most 2^100
+        float scale = acc.y * r / kE4m3Max;
+        inv = kE4m3Max / acc.y;  // r is in both
+        if (r != r) {
+            scale = inv = r;
+        } else if (!(scale >= kScaleMin)) {
+            scale = kScaleMin;
+            inv = fminf(r * (1.f / kScaleMin), 3e38f);
+        }
         if (threadIdx.x == 0) p.scale[row] = scale;
     }
 #pragma unroll
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(1024) ttt_rmsnorm_kernel(const NormParams p) {
             if (p.h) store_vec<V>(static_cast<T*>(p.h) + base + j, h[i]);
             float y[V];
 #pragma unroll
-            for (int k = 0; k < V; k++) y[k] = kQ8 ? g[i][k] * r * inv : g[i][k] * r;
+            for (int k = 0; k < V; k++) y[k] = g[i][k] * (kQ8 ? inv : r);
             if constexpr (!kQ8) {
                 store_vec<V>(static_cast<T*>(p.y) + base + j, y);
             } else {
