@@ -494,23 +494,24 @@ class _Launch:
     """Device and stream of one call: makes the tensors' device current and, where a stream is given, allocates
     on it, so that the caching allocator knows which stream the call's buffers are used on."""
 
+    __slots__ = ("dev", "entered", "stream")
+
     def __init__(self, dev: torch.device, stream):
-        self.device = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-        self.stream = None if stream is None else torch.cuda.stream(_launch_stream(dev, stream))
-        self.dev = dev
+        self.dev, self.stream, self.entered = dev, stream, ()
 
     def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
+        dev = self.dev
+        if dev.index != torch.cuda.current_device():
+            self.entered = (torch.cuda.device(dev),)
         if self.stream is not None:
-            self.stream.__enter__()
-        return torch.cuda.current_stream(self.dev).cuda_stream
+            self.entered += (torch.cuda.stream(_launch_stream(dev, self.stream)),)
+        for c in self.entered:
+            c.__enter__()
+        return torch._C._cuda_getCurrentRawStream(dev.index)  # current_stream(dev).cuda_stream, 4 us cheaper
 
     def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+        for c in reversed(self.entered):
+            c.__exit__(*exc)
 
 
 def _token_dtype(t: torch.Tensor, name: str) -> int:
@@ -525,9 +526,9 @@ def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> Optional[
     """Address of a contiguous CUDA tensor of this shape, type and device (None for None)."""
     if t is None:
         return None
-    if t.device != dev or not t.is_cuda or not t.is_contiguous():
+    if t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -538,9 +539,9 @@ def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
     """(address, row stride) of token rows [B, T, width], which may be a slice of wider rows."""
     if t is None:
         return None, 0
-    if t.device != dev or not t.is_cuda:
+    if t.get_device() != dev.index:
         raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -556,7 +557,7 @@ def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
 def _workspace(given: Optional[torch.Tensor], need: int, dev):
     if given is None:
         given = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif given.device != dev or not given.is_contiguous():
+    elif given.get_device() != dev.index or not given.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
     return given, given.data_ptr(), given.numel() * given.element_size()
 

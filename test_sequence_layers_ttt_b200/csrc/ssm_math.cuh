@@ -11,7 +11,7 @@
 // (16 a clock an SM), which stays the bound.
 #pragma once
 
-#include "common.cuh"
+#include "vec_io.cuh"
 
 namespace ttt {
 namespace ssm {
@@ -19,12 +19,6 @@ namespace ssm {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSmall = 0.0625f;
 constexpr float kQ0 = 0x1.62e42ep-1f, kQ1 = 0x1.ebf0e6p-3f, kQ2 = 0x1.bf5dd8p-5f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 __device__ __forceinline__ float decay(float x) {
     const float q = fmaf(fmaf(kQ2, x, kQ1), x, kQ0);
@@ -36,7 +30,7 @@ __device__ __forceinline__ float decay(float x) {
 // (0, 1/3], by an even polynomial that fits 2 atanh(s) / s to 8e-9; right to a few 1e-7 of the result at any x.
 __device__ __forceinline__ float softplus(float x) {
     const float e = ex2(-kLog2e * fabsf(x));
-    const float s = __fdividef(e, 2.f + e), w = s * s;
+    const float s = e * rcp(2.f + e), w = s * s;
     float p = 0x1.208bd0p-2f;
     p = fmaf(p, w, 0x1.1e510ap-2f);
     p = fmaf(p, w, 0x1.99dae6p-2f);
@@ -65,15 +59,33 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-__device__ __forceinline__ f2 decay2(f2 x) {
-    const f2 q = fma2(fma2(pack2(kQ2, kQ2), x, pack2(kQ1, kQ1)), x, pack2(kQ0, kQ0));
-    const f2 near_one = fma2(q, x, pack2(1.f, 1.f));
-    float x0, x1, n0, n1;
-    unpack2(x, x0, x1);
-    unpack2(near_one, n0, n1);
-    if (!(fabsf(x0) < kSmall)) n0 = ex2(x0);
-    if (!(fabsf(x1) < kSmall)) n1 = ex2(x1);
-    return pack2(n0, n1);
+// 2^x in the place of `near_one` where |x| >= 1/16: one comparison and a predicated instruction
+__device__ __forceinline__ void ex2_beyond(float& near_one, float x) {
+    asm("{\n .reg .pred p;\n .reg .f32 m;\n abs.f32 m, %1;\n setp.ge.f32 p, m, 0f3D800000;\n"
+        " @p ex2.approx.ftz.f32 %0, %1;\n}"
+        : "+f"(near_one)
+        : "f"(x));
+}
+// decay() of 2 kPairs values, x in pairs; step by step over all pairs, so that a warp has independent work
+// at every step
+template <int kPairs>
+__device__ __forceinline__ void decays(float (&a)[2 * kPairs], const f2 (&x)[kPairs]) {
+    const f2 c2 = pack2(kQ2, kQ2), c1 = pack2(kQ1, kQ1), c0 = pack2(kQ0, kQ0), one = pack2(1.f, 1.f);
+    f2 q[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; i++) q[i] = fma2(c2, x[i], c1);
+#pragma unroll
+    for (int i = 0; i < kPairs; i++) q[i] = fma2(q[i], x[i], c0);
+#pragma unroll
+    for (int i = 0; i < kPairs; i++) q[i] = fma2(q[i], x[i], one);
+#pragma unroll
+    for (int i = 0; i < kPairs; i++) {
+        float x0, x1;
+        unpack2(x[i], x0, x1);
+        unpack2(q[i], a[2 * i], a[2 * i + 1]);
+        ex2_beyond(a[2 * i], x0);
+        ex2_beyond(a[2 * i + 1], x1);
+    }
 }
 
 __device__ __forceinline__ int length_of(const int* lengths, int b, int T) {

@@ -7,9 +7,10 @@
 //   dx_t = sum_j w_j dp_{t + W - 1 - j},  dw_j = sum_t dp_t x_{t - (W - 1) + j},  dbias = sum_t dp_t
 // and the gradient of the last W - 1 rows gets that of the final state added.
 //
-// Bound by HBM (forward: a row read and a row written).  A thread owns V neighbouring channels (16
-// bytes; 8 in the backward) and walks a piece of the tokens with the last W - 1 rows in registers, so a
-// row is read once but for the W - 1 rows before each piece.  Sums are in fp32, rounded once.
+// Bound by HBM (forward: a row read and a row written).  A thread owns V = 4 neighbouring channels (1
+// where rows do not allow it) and walks a piece of the tokens with the last W - 1 rows in registers and
+// the next rows on their way, so a row is read once but for the W - 1 rows before each piece.  Sums are in
+// fp32, rounded once.
 #include "block_internal.h"
 #include "vec_io.cuh"
 
@@ -33,7 +34,7 @@ struct ConvParams {
 };
 
 constexpr int kThreads = 128;
-constexpr int kRows = 4;  // rows loaded ahead of their use
+constexpr int kAhead = 8;  // rows on their way while the ones before them are worked on
 
 // Row t of the window of sequence b (t < 0: the state's rows), the thread's channels.
 template <typename T, int V, int W>
@@ -84,25 +85,27 @@ __global__ void __launch_bounds__(kThreads) ttt_conv_kernel(const ConvParams p) 
 #pragma unroll
         for (int i = 0; i < W - 1; i++) store_vec<V>(out + (long long)i * p.C, last[i]);
     }
+    Raw<T, V> next[kAhead];
+#pragma unroll
+    for (int r = 0; r < kAhead; r++)
+        if (t0 + r < live) next[r].load(x + (long long)(t0 + r) * p.ld);
     int t = t0;
-    for (; t < live; t += kRows) {
-        float in[kRows][V];
+    for (; t < live; t += kAhead) {
 #pragma unroll
-        for (int r = 0; r < kRows; r++)
-            if (t + r < live) load_vec<V>(x + (long long)(t + r) * p.ld, in[r]);
-#pragma unroll
-        for (int r = 0; r < kRows; r++) {
+        for (int r = 0; r < kAhead; r++) {
             if (t + r < live) {
-                float o[V];
+                float in[V], o[V];
+                next[r].get(in);
+                if (t + kAhead + r < live) next[r].load(x + (long long)(t + kAhead + r) * p.ld);
 #pragma unroll
                 for (int k = 0; k < V; k++) {
                     float a = bias[k];
 #pragma unroll
                     for (int j = 0; j < W - 1; j++) a += w[j][k] * win[j][k];
-                    a += w[W - 1][k] * in[r][k];
+                    a += w[W - 1][k] * in[k];
 #pragma unroll
                     for (int j = 0; j + 1 < W - 1; j++) win[j][k] = win[j + 1][k];
-                    win[W - 2][k] = in[r][k];
+                    win[W - 2][k] = in[k];
                     o[k] = p.silu ? a * sigmoid(a) : a;
                 }
                 store_vec<V>(y + (long long)(t + r) * p.C, o);
@@ -126,6 +129,7 @@ struct ConvBwdParams {
     int silu;
 };
 
+constexpr int kBack = 4;  // rows of x and dy on their way
 constexpr int kLanes = 32, kSub = 4;  // threads: 32 channel vectors x 4 runs of a piece's tokens
 
 template <typename T, int V, int W>
@@ -174,14 +178,30 @@ __global__ void __launch_bounds__(kLanes * kSub) ttt_conv_backward_kernel(const 
         }
         // step t: dp_t is computed, and with it row t - (W - 1) is complete
         if (t0 < t1 || (t0 == 0 && p.T == 0)) {
-            for (int t = t0; t < t1 + W - 1; t++) {
+            const int stop = t1 + W - 1, live = min(stop, n);
+            Raw<T, V> next_x[kBack], next_g[kBack];
+#pragma unroll
+            for (int q = 0; q < kBack; q++)
+                if (t0 + q < live) {
+                    next_x[q].load(x + (long long)(t0 + q) * p.ld);
+                    next_g[q].load(dy + (long long)(t0 + q) * p.C);
+                }
+            for (int tq = t0; tq < stop; tq += kBack)
+#pragma unroll
+            for (int q = 0; q < kBack; q++) {
+                const int t = tq + q;
+                if (t >= stop) break;
                 float now[V];
 #pragma unroll
                 for (int k = 0; k < V; k++) now[k] = 0.f;
-                if (t < n) {
+                if (t < live) {
                     float in[V], g[V];
-                    load_vec<V>(x + (long long)t * p.ld, in);
-                    load_vec<V>(dy + (long long)t * p.C, g);
+                    next_x[q].get(in);
+                    next_g[q].get(g);
+                    if (t + kBack < live) {
+                        next_x[q].load(x + (long long)(t + kBack) * p.ld);
+                        next_g[q].load(dy + (long long)(t + kBack) * p.C);
+                    }
 #pragma unroll
                     for (int k = 0; k < V; k++) {
                         float a = bias[k];
@@ -295,8 +315,8 @@ int forward_piece(const ConvArgs& a, int vec) {
 
 template <typename T>
 cudaError_t forward(const ConvArgs& a, cudaStream_t stream) {
-    constexpr int kV = Elem<T>::kVec;
-    const bool vec = a.C % kV == 0 && rows_aligned(a.x, a.ld, 16, sizeof(T));
+    constexpr int kV = 4;
+    const bool vec = a.C % kV == 0 && rows_aligned(a.x, a.ld, kV * sizeof(T), sizeof(T));
     const int v = vec ? kV : 1;
     ConvParams p{};
     p.T = a.T;

@@ -12,16 +12,12 @@
 // of one, so that B and C are one broadcast read each; the warps of a block share out the states.  Sums
 // over states meet in shared memory, sums over the block's channels in shuffles; what is summed over
 // blocks or sequences goes through the workspace and is added up in an order that the shape fixes.
-#include "block_internal.h"
-#include "ssm_math.cuh"
-#include "vec_io.cuh"
+#include "ssm_params.cuh"
 
 namespace ttt {
 namespace {
 
 using namespace ssm;
-
-constexpr int kS = 4;  // states a thread
 
 struct SsmBwdParams {
     int B, T, C, N, chunks, cblocks;
@@ -45,73 +41,111 @@ __device__ __forceinline__ Where where(int cblocks) {
     return {(int)(blockIdx.x / cblocks), (int)(blockIdx.x % cblocks) * 32};
 }
 
+// Rows of a tile of kK tokens as they come from memory
+template <typename T, int kK, int kNp>
+struct RawTile {
+    T u[kK][32], dt[kK][32], z[kK][32], dy[kK][32];
+    T b[kK][kNp], c[kK][kNp];
+};
+
 // ---------------------------------------------------------------- pass 1: the states at the chunks' starts
-template <typename T, int kNW, int kK>
+template <typename T, int kNW, int kTile>
+struct CkptSmem {
+    RawTile<T, kTile, kStates * kNW> raw[2];
+    float4 dt[kTile / 4][32], du[kTile / 4][32];
+    float b[kStates * kNW][kTile + 4];
+};
+
+// kK: tokens of a chunk; a tile is two chunks
+template <typename T, int kNW, int kK, bool kVecRows, bool kVecBC>
 __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmBwdParams p) {
-    constexpr int kNp = kS * kNW;                        // states, padded
-    constexpr int kPairs = kK / kNW > 0 ? kK / kNW : 1;  // (token, channel) pairs a thread prepares
-    __shared__ float2 s_dt[2][kK][32];                   // dt, dt u
-    __shared__ __align__(16) float s_b[2][kK][kNp];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kNp = kStates * kNW, kTile = 2 * kK, kThreads = 32 * kNW;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    CkptSmem<T, kNW, kTile>& s = *reinterpret_cast<CkptSmem<T, kNW, kTile>*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Where w = where(p.cblocks);
     const int c = w.c0 + lane;
     const bool on = c < p.C;
     const int len = length_of(p.lengths, w.b, p.T);
-    const int n_chunks = (len + kK - 1) / kK;
-    const int n0 = warp * kS;
-    float h[kS], a2[kS];
+    const int n_chunks = (len + kK - 1) / kK, tiles = (len + kTile - 1) / kTile;
+    const int n0 = warp * kStates;
+    float h[kStates], a2[kStates];
 #pragma unroll
-    for (int i = 0; i < kS; i++) {
+    for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N;
         a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
         h[i] = live && p.h0 ? p.h0[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
     }
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f;
-
-    const auto fill = [&](int chunk, int buf) {
-#pragma unroll
-        for (int j = 0; j < kPairs; j++) {
-            const int k = warp + j * kNW, t = chunk * kK + k;
-            if (k < kK) {
-                float dt = 0.f, du = 0.f;
-                if (on && t < len) {
-                    const long long row = (long long)w.b * p.T + t;
-                    dt = to_f32(static_cast<const T*>(p.dt)[row * p.ld_dt + c]) + bias;
-                    if (p.softplus) dt = ssm::softplus(dt);
-                    du = dt * to_f32(static_cast<const T*>(p.u)[row * p.ld_u + c]);
-                }
-                s_dt[buf][k][lane] = make_float2(dt, du);
-            }
-        }
-        for (int i = threadIdx.x; i < kK * kNp; i += 32 * kNW) {
-            const int k = i / kNp, n = i % kNp, t = chunk * kK + k;
-            float v = 0.f;
-            if (t < len && n < p.N) v = to_f32(static_cast<const T*>(p.Bm)[((long long)w.b * p.T + t) * p.ld_b + n]);
-            s_b[buf][k][n] = v;
-        }
+    const long long row0 = (long long)w.b * p.T;
+    const auto stage = [&](int m) {
+        RawTile<T, kTile, kNp>& r = s.raw[m & 1];
+        const int t0 = m * kTile, width = p.C - w.c0;
+        stage_rows<T, kVecRows>(&r.u[0][0], static_cast<const T*>(p.u) + row0 * p.ld_u + w.c0, p.ld_u, t0, kTile, len, 32, width, tid, kThreads);
+        stage_rows<T, kVecRows>(&r.dt[0][0], static_cast<const T*>(p.dt) + row0 * p.ld_dt + w.c0, p.ld_dt, t0, kTile, len, 32, width, tid, kThreads);
+        stage_rows<T, kVecBC>(&r.b[0][0], static_cast<const T*>(p.Bm) + row0 * p.ld_b, p.ld_b, t0, kTile, len, kNp, p.N, tid, kThreads);
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-
-    if (n_chunks > 0) fill(0, 0);
-    __syncthreads();
-    for (int chunk = 0; chunk < n_chunks; chunk++) {
-        const int buf = chunk & 1;
-        if (on) {
-            float* out = p.ckpt + (((size_t)w.b * p.chunks + chunk) * kNp + n0) * p.C + c;
+    if (tiles > 0) stage(0);
+    for (int m = 0; m < tiles; m++) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        if (m + 1 < tiles) stage(m + 1);
+        const RawTile<T, kTile, kNp>& r = s.raw[m & 1];
+        for (int q = warp; q < kTile / 4; q += kNW) {
+            float dt[4], du[4];
 #pragma unroll
-            for (int i = 0; i < kS; i++) out[(size_t)i * p.C] = h[i];
+            for (int k = 0; k < 4; k++) {
+                const float raw = to_f32(r.dt[4 * q + k][lane]) + bias;
+                dt[k] = m * kTile + 4 * q + k < len ? (p.softplus ? ssm::softplus(raw) : raw) : 0.f;
+                du[k] = dt[k] * to_f32(r.u[4 * q + k][lane]);
+            }
+            s.dt[q][lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+            s.du[q][lane] = make_float4(du[0], du[1], du[2], du[3]);
         }
-        if (chunk + 1 < n_chunks) {
-            fill(chunk + 1, buf ^ 1);
+        for (int i = tid; i < kTile * kNp; i += kThreads) s.b[i % kNp][i / kNp] = to_f32(r.b[i / kNp][i % kNp]);
+        __syncthreads();
 #pragma unroll
-            for (int k = 0; k < kK; k++) {
-                const float2 d = s_dt[buf][k][lane];
-                const float4 Bt = *reinterpret_cast<const float4*>(&s_b[buf][k][n0]);
-                const float bt[kS] = {Bt.x, Bt.y, Bt.z, Bt.w};
+        for (int half = 0; half < 2; half++) {
+            const int chunk = 2 * m + half;
+            if (on && chunk < n_chunks) {
+                float* out = p.ckpt + (((size_t)w.b * p.chunks + chunk) * kNp + n0) * p.C + c;
 #pragma unroll
-                for (int i = 0; i < kS; i++) h[i] = fmaf(decay(d.x * a2[i]), h[i], d.y * bt[i]);
+                for (int i = 0; i < kStates; i++) out[(size_t)i * p.C] = h[i];
+            }
+            constexpr int kQ = kK / 4;
+            f2 dt[2 * kQ], du[2 * kQ];
+#pragma unroll
+            for (int q = 0; q < kQ; q++) {
+                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s.dt[half * kQ + q][lane]);
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(&s.du[half * kQ + q][lane]);
+                dt[2 * q] = d.x;
+                dt[2 * q + 1] = d.y;
+                du[2 * q] = e.x;
+                du[2 * q + 1] = e.y;
+            }
+#pragma unroll
+            for (int i = 0; i < kStates; i++) {
+                const f2 A2 = pack2(a2[i], a2[i]);
+                f2 x[2 * kQ];
+                float a[4 * kQ];
+#pragma unroll
+                for (int k = 0; k < 2 * kQ; k++) x[k] = mul2(dt[k], A2);
+                decays<2 * kQ>(a, x);
+                const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][half * kK]);
+#pragma unroll
+                for (int q = 0; q < kQ; q++) {
+                    const ulonglong2 Bq = Bi[q];
+                    float v0, v1, v2, v3;
+                    unpack2(mul2(du[2 * q], Bq.x), v0, v1);
+                    unpack2(mul2(du[2 * q + 1], Bq.y), v2, v3);
+                    h[i] = fmaf(a[4 * q], h[i], v0);
+                    h[i] = fmaf(a[4 * q + 1], h[i], v1);
+                    h[i] = fmaf(a[4 * q + 2], h[i], v2);
+                    h[i] = fmaf(a[4 * q + 3], h[i], v3);
+                }
             }
         }
-        __syncthreads();
     }
 }
 
@@ -131,32 +165,33 @@ __device__ __forceinline__ float sum_scatter(float (&v)[32], int lane) {
     return v[0];
 }
 
-template <int kNW, int kK>
+template <typename T, int kNW, int kK>
 struct BwdSmem {
-    float b[kK][kS * kNW], c[kK][kS * kNW];
-    float2 dt[kK][32];  // dt, dt u
-    float dy[kK][32];   // dy'
-    float gb[kNW][kK][32], ga[kNW][kK][32], y[kNW][kK][32];
+    RawTile<T, kK, kStates * kNW> raw[2];
+    float b[kStates * kNW][kK + 4], c[kStates * kNW][kK + 4];
+    float4 dt[kK / 4][32], du[kK / 4][32], dy[kK / 4][32];  // dt, dt u, dy'
+    float4 slope[kK / 4][32], dyz[kK / 4][32];              // d dt / d raw, dy silu'(z)
+    float4 gb[kNW][kK / 4][32], ga[kNW][kK / 4][32], y[kNW][kK / 4][32];
     float sum[kNW][2][32];
 };
 
-template <typename T, int kNW, int kK>
+template <typename T, int kNW, int kK, bool kVecRows, bool kVecBC>
 __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwdParams p) {
-    constexpr int kNp = kS * kNW;
-    constexpr int kPairs = kK / kNW > 0 ? kK / kNW : 1;
+    constexpr int kNp = kStates * kNW, kQ = kK / 4, kThreads = 32 * kNW;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    BwdSmem<kNW, kK>& s = *reinterpret_cast<BwdSmem<kNW, kK>*>(smem_raw);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    BwdSmem<T, kNW, kK>& s = *reinterpret_cast<BwdSmem<T, kNW, kK>*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Where w = where(p.cblocks);
     const int cblk = (int)(blockIdx.x % p.cblocks);
     const int c = w.c0 + lane;
     const bool on = c < p.C;
     const int len = length_of(p.lengths, w.b, p.T);
     const int n_chunks = (len + kK - 1) / kK;
-    const int n0 = warp * kS;
-    float a2[kS], g[kS], dA[kS];
+    const int n0 = warp * kStates;
+    const long long row0 = (long long)w.b * p.T;
+    float a2[kStates], g[kStates], dA[kStates], first[kStates];
 #pragma unroll
-    for (int i = 0; i < kS; i++) {
+    for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N;
         a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
         g[i] = live && p.dh_T ? p.dh_T[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
@@ -168,7 +203,7 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
     // rows of padding: zero gradients
     for (int t = len + warp; t < p.T; t += kNW) {
         if (on) {
-            const size_t at = ((size_t)w.b * p.T + t) * p.C + c;
+            const size_t at = ((size_t)row0 + t) * p.C + c;
             const float zero[1] = {0.f};
             store_vec<1>(static_cast<T*>(p.du) + at, zero);
             store_vec<1>(static_cast<T*>(p.ddt) + at, zero);
@@ -176,110 +211,171 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
         }
     }
 
+    const auto stage = [&](int chunk) {
+        RawTile<T, kK, kNp>& r = s.raw[chunk & 1];
+        const int t0 = chunk * kK, width = p.C - w.c0;
+        stage_rows<T, kVecRows>(&r.u[0][0], static_cast<const T*>(p.u) + row0 * p.ld_u + w.c0, p.ld_u, t0, kK, len, 32, width, tid, kThreads);
+        stage_rows<T, kVecRows>(&r.dt[0][0], static_cast<const T*>(p.dt) + row0 * p.ld_dt + w.c0, p.ld_dt, t0, kK, len, 32, width, tid, kThreads);
+        stage_rows<T, kVecRows>(&r.dy[0][0], static_cast<const T*>(p.dy) + row0 * p.C + w.c0, p.C, t0, kK, len, 32, width, tid, kThreads);
+        if (p.z)
+            stage_rows<T, kVecRows>(&r.z[0][0], static_cast<const T*>(p.z) + row0 * p.ld_z + w.c0, p.ld_z, t0, kK, len, 32, width, tid, kThreads);
+        stage_rows<T, kVecBC>(&r.b[0][0], static_cast<const T*>(p.Bm) + row0 * p.ld_b, p.ld_b, t0, kK, len, kNp, p.N, tid, kThreads);
+        stage_rows<T, kVecBC>(&r.c[0][0], static_cast<const T*>(p.Cm) + row0 * p.ld_c, p.ld_c, t0, kK, len, kNp, p.N, tid, kThreads);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const auto load_first = [&](int chunk) {
+        const float* in = p.ckpt + (((size_t)w.b * p.chunks + chunk) * kNp + n0) * p.C + c;
+#pragma unroll
+        for (int i = 0; i < kStates; i++) first[i] = on ? in[(size_t)i * p.C] : 0.f;
+    };
+    if (n_chunks > 0) {
+        stage(n_chunks - 1);
+        load_first(n_chunks - 1);
+    }
     for (int chunk = n_chunks - 1; chunk >= 0; chunk--) {
-        float u[kPairs], dt[kPairs], slope[kPairs], dyg[kPairs], dyz[kPairs];
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        if (chunk > 0) stage(chunk - 1);
+        const RawTile<T, kK, kNp>& r = s.raw[chunk & 1];
+        for (int q = warp; q < kQ; q += kNW) {
+            float dt[4], du[4], dy[4], slope[4], dyz[4];
 #pragma unroll
-        for (int j = 0; j < kPairs; j++) {
-            const int k = warp + j * kNW, t = chunk * kK + k;
-            u[j] = dt[j] = slope[j] = dyg[j] = dyz[j] = 0.f;
-            if (k < kK) {
-                if (on && t < len) {
-                    const long long row = (long long)w.b * p.T + t;
-                    const float raw = to_f32(static_cast<const T*>(p.dt)[row * p.ld_dt + c]) + bias;
-                    u[j] = to_f32(static_cast<const T*>(p.u)[row * p.ld_u + c]);
-                    dt[j] = p.softplus ? ssm::softplus(raw) : raw;
-                    slope[j] = p.softplus ? sigmoid(raw) : 1.f;
-                    dyg[j] = to_f32(static_cast<const T*>(p.dy)[row * p.C + c]);
-                    if (p.z) {
-                        const float z = to_f32(static_cast<const T*>(p.z)[row * p.ld_z + c]), sg = sigmoid(z);
-                        dyz[j] = dyg[j] * sg * (1.f + z * (1.f - sg));
-                        dyg[j] *= z * sg;
-                    }
+            for (int k = 0; k < 4; k++) {
+                const int j = 4 * q + k;
+                const bool live = chunk * kK + j < len;
+                const float raw = to_f32(r.dt[j][lane]) + bias;
+                dt[k] = live ? (p.softplus ? ssm::softplus(raw) : raw) : 0.f;
+                slope[k] = p.softplus ? sigmoid(raw) : 1.f;
+                du[k] = dt[k] * to_f32(r.u[j][lane]);
+                dy[k] = to_f32(r.dy[j][lane]);
+                dyz[k] = 0.f;
+                if (p.z) {
+                    const float z = to_f32(r.z[j][lane]), sg = sigmoid(z);
+                    dyz[k] = dy[k] * sg * (1.f + z * (1.f - sg));
+                    dy[k] *= z * sg;
                 }
-                s.dt[k][lane] = make_float2(dt[j], dt[j] * u[j]);
-                s.dy[k][lane] = dyg[j];
             }
+            s.dt[q][lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+            s.du[q][lane] = make_float4(du[0], du[1], du[2], du[3]);
+            s.dy[q][lane] = make_float4(dy[0], dy[1], dy[2], dy[3]);
+            s.slope[q][lane] = make_float4(slope[0], slope[1], slope[2], slope[3]);
+            s.dyz[q][lane] = make_float4(dyz[0], dyz[1], dyz[2], dyz[3]);
         }
-        for (int i = threadIdx.x; i < kK * kNp; i += 32 * kNW) {
-            const int k = i / kNp, n = i % kNp, t = chunk * kK + k;
-            const bool live = t < len && n < p.N;
-            const long long row = (long long)w.b * p.T + t;
-            s.b[k][n] = live ? to_f32(static_cast<const T*>(p.Bm)[row * p.ld_b + n]) : 0.f;
-            s.c[k][n] = live ? to_f32(static_cast<const T*>(p.Cm)[row * p.ld_c + n]) : 0.f;
-        }
-        float a[kK][kS], h[kK + 1][kS];
-        {
-            const float* in = p.ckpt + (((size_t)w.b * p.chunks + chunk) * kNp + n0) * p.C + c;
-#pragma unroll
-            for (int i = 0; i < kS; i++) h[0][i] = on ? in[(size_t)i * p.C] : 0.f;
+        for (int i = tid; i < kK * kNp; i += kThreads) {
+            s.b[i % kNp][i / kNp] = to_f32(r.b[i / kNp][i % kNp]);
+            s.c[i % kNp][i / kNp] = to_f32(r.c[i / kNp][i % kNp]);
         }
         __syncthreads();
+        float a[kStates][kK], h[kStates][kK + 1];
+        {
+            f2 dt[2 * kQ], du[2 * kQ];
 #pragma unroll
-        for (int k = 0; k < kK; k++) {
-            const float2 d = s.dt[k][lane];
-            const float4 Bt = *reinterpret_cast<const float4*>(&s.b[k][n0]);
-            const float bt[kS] = {Bt.x, Bt.y, Bt.z, Bt.w};
+            for (int q = 0; q < kQ; q++) {
+                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s.dt[q][lane]);
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(&s.du[q][lane]);
+                dt[2 * q] = d.x;
+                dt[2 * q + 1] = d.y;
+                du[2 * q] = e.x;
+                du[2 * q + 1] = e.y;
+            }
 #pragma unroll
-            for (int i = 0; i < kS; i++) {
-                a[k][i] = decay(d.x * a2[i]);
-                h[k + 1][i] = fmaf(a[k][i], h[k][i], d.y * bt[i]);
+            for (int i = 0; i < kStates; i++) {
+                const f2 A2 = pack2(a2[i], a2[i]);
+                f2 x[2 * kQ];
+#pragma unroll
+                for (int k = 0; k < 2 * kQ; k++) x[k] = mul2(dt[k], A2);
+                decays<2 * kQ>(a[i], x);
+                const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][0]);
+                h[i][0] = first[i];
+#pragma unroll
+                for (int q = 0; q < kQ; q++) {
+                    const ulonglong2 Bq = Bi[q];
+                    float v[4];
+                    unpack2(mul2(du[2 * q], Bq.x), v[0], v[1]);
+                    unpack2(mul2(du[2 * q + 1], Bq.y), v[2], v[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) h[i][4 * q + k + 1] = fmaf(a[i][4 * q + k], h[i][4 * q + k], v[k]);
+                }
             }
         }
+        if (chunk > 0) load_first(chunk - 1);
 #pragma unroll
-        for (int k4 = kK - 4; k4 >= 0; k4 -= 4) {
+        for (int q = kQ - 1; q >= 0; q--) {
             float v[32];  // of four tokens: dB and dC of the thread's four states
+            const ulonglong2 dt = *reinterpret_cast<const ulonglong2*>(&s.dt[q][lane]);
+            const ulonglong2 du = *reinterpret_cast<const ulonglong2*>(&s.du[q][lane]);
+            const ulonglong2 dy = *reinterpret_cast<const ulonglong2*>(&s.dy[q][lane]);
+            float d[4];
+            unpack2(dy.x, d[0], d[1]);
+            unpack2(dy.y, d[2], d[3]);
+            f2 gb[2], ga[2], y[2];
 #pragma unroll
-            for (int q = 3; q >= 0; q--) {
-                const int k = k4 + q;
-                const float2 d = s.dt[k][lane];
-                const float dyk = s.dy[k][lane];
-                const float4 Bt = *reinterpret_cast<const float4*>(&s.b[k][n0]);
-                const float4 Ct = *reinterpret_cast<const float4*>(&s.c[k][n0]);
-                const float bt[kS] = {Bt.x, Bt.y, Bt.z, Bt.w}, ct[kS] = {Ct.x, Ct.y, Ct.z, Ct.w};
-                float gb = 0.f, ga = 0.f, y = 0.f;
+            for (int i = 0; i < kStates; i++) {
+                const ulonglong2 Bq = *reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][4 * q]);
+                const ulonglong2 Cq = *reinterpret_cast<const ulonglong2*>(&s.c[n0 + i][4 * q]);
+                float ct[4], gk[4], x[4];
+                unpack2(Cq.x, ct[0], ct[1]);
+                unpack2(Cq.y, ct[2], ct[3]);
 #pragma unroll
-                for (int i = 0; i < kS; i++) {
-                    g[i] = fmaf(ct[i], dyk, g[i]);
-                    v[q * 8 + i] = g[i] * d.y;
-                    v[q * 8 + 4 + i] = dyk * h[k + 1][i];
-                    gb = fmaf(g[i], bt[i], gb);
-                    y = fmaf(ct[i], h[k + 1][i], y);
-                    g[i] *= a[k][i];
-                    const float x = g[i] * h[k][i];
-                    ga = fmaf(x, a2[i], ga);
-                    dA[i] = fmaf(x, d.x, dA[i]);
+                for (int k = 3; k >= 0; k--) {
+                    gk[k] = fmaf(ct[k], d[k], g[i]);
+                    g[i] = gk[k] * a[i][4 * q + k];
+                    x[k] = g[i] * h[i][4 * q + k];
                 }
-                s.gb[warp][k][lane] = gb;
-                s.ga[warp][k][lane] = ga;
-                s.y[warp][k][lane] = y;
+                const f2 g0 = pack2(gk[0], gk[1]), g1 = pack2(gk[2], gk[3]);
+                const f2 h0 = pack2(h[i][4 * q + 1], h[i][4 * q + 2]), h1 = pack2(h[i][4 * q + 3], h[i][4 * q + 4]);
+                const f2 x0 = pack2(x[0], x[1]), x1 = pack2(x[2], x[3]), A2 = pack2(a2[i], a2[i]);
+                unpack2(mul2(g0, du.x), v[i], v[8 + i]);
+                unpack2(mul2(g1, du.y), v[16 + i], v[24 + i]);
+                unpack2(mul2(dy.x, h0), v[4 + i], v[12 + i]);
+                unpack2(mul2(dy.y, h1), v[20 + i], v[28 + i]);
+                gb[0] = i == 0 ? mul2(g0, Bq.x) : fma2(g0, Bq.x, gb[0]);
+                gb[1] = i == 0 ? mul2(g1, Bq.y) : fma2(g1, Bq.y, gb[1]);
+                y[0] = i == 0 ? mul2(h0, Cq.x) : fma2(h0, Cq.x, y[0]);
+                y[1] = i == 0 ? mul2(h1, Cq.y) : fma2(h1, Cq.y, y[1]);
+                ga[0] = i == 0 ? mul2(x0, A2) : fma2(x0, A2, ga[0]);
+                ga[1] = i == 0 ? mul2(x1, A2) : fma2(x1, A2, ga[1]);
+                float lo, hi;
+                unpack2(fma2(x1, dt.y, mul2(x0, dt.x)), lo, hi);
+                dA[i] += lo + hi;
             }
+            *reinterpret_cast<ulonglong2*>(&s.gb[warp][q][lane]) = make_ulonglong2(gb[0], gb[1]);
+            *reinterpret_cast<ulonglong2*>(&s.ga[warp][q][lane]) = make_ulonglong2(ga[0], ga[1]);
+            *reinterpret_cast<ulonglong2*>(&s.y[warp][q][lane]) = make_ulonglong2(y[0], y[1]);
             const float sum = sum_scatter(v, lane);
-            const int t = chunk * kK + k4 + (lane >> 3), n = n0 + (lane & 3);
+            const int t = chunk * kK + 4 * q + (lane >> 3), n = n0 + (lane & 3);
             if (t < len && n < p.N)
                 p.part_bc[((((size_t)cblk * p.B + w.b) * p.T + t) * 2 + ((lane >> 2) & 1)) * p.N + n] = sum;
         }
         __syncthreads();
+        for (int q = warp; q < kQ; q += kNW) {
+            float4 gb = s.gb[0][q][lane], ga = s.ga[0][q][lane], y = s.y[0][q][lane];
 #pragma unroll
-        for (int j = 0; j < kPairs; j++) {
-            const int k = warp + j * kNW, t = chunk * kK + k;
-            if (k < kK && on && t < len) {
-                float gb = 0.f, ga = 0.f, y = 0.f;
+            for (int k = 1; k < kNW; k++) {
+                const float4 b4 = s.gb[k][q][lane], a4 = s.ga[k][q][lane], y4 = s.y[k][q][lane];
+                gb = make_float4(gb.x + b4.x, gb.y + b4.y, gb.z + b4.z, gb.w + b4.w);
+                ga = make_float4(ga.x + a4.x, ga.y + a4.y, ga.z + a4.z, ga.w + a4.w);
+                y = make_float4(y.x + y4.x, y.y + y4.y, y.z + y4.z, y.w + y4.w);
+            }
+            const float4 dt4 = s.dt[q][lane], dy4 = s.dy[q][lane], sl4 = s.slope[q][lane], dz4 = s.dyz[q][lane];
+            const float gbs[4] = {gb.x, gb.y, gb.z, gb.w}, gas[4] = {ga.x, ga.y, ga.z, ga.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            const float dts[4] = {dt4.x, dt4.y, dt4.z, dt4.w}, dys[4] = {dy4.x, dy4.y, dy4.z, dy4.w};
+            const float sls[4] = {sl4.x, sl4.y, sl4.z, sl4.w}, dzs[4] = {dz4.x, dz4.y, dz4.z, dz4.w};
 #pragma unroll
-                for (int q = 0; q < kNW; q++) {
-                    gb += s.gb[q][k][lane];
-                    ga += s.ga[q][k][lane];
-                    y += s.y[q][k][lane];
-                }
-                const size_t at = ((size_t)w.b * p.T + t) * p.C + c;
-                const float o_u[1] = {fmaf(dt[j], gb, skip * dyg[j])};
-                const float o_dt[1] = {fmaf(u[j], gb, ga * (1.f / kLog2e)) * slope[j]};
+            for (int k = 0; k < 4; k++) {
+                const int t = chunk * kK + 4 * q + k;
+                if (!on || t >= len) continue;
+                const float u = to_f32(r.u[4 * q + k][lane]);
+                const size_t at = ((size_t)row0 + t) * p.C + c;
+                const float o_u[1] = {fmaf(dts[k], gbs[k], skip * dys[k])};
+                const float o_dt[1] = {fmaf(u, gbs[k], gas[k] * (1.f / kLog2e)) * sls[k]};
                 store_vec<1>(static_cast<T*>(p.du) + at, o_u);
                 store_vec<1>(static_cast<T*>(p.ddt) + at, o_dt);
                 if (p.dz) {
-                    const float o_z[1] = {dyz[j] * fmaf(skip, u[j], y)};
+                    const float o_z[1] = {dzs[k] * fmaf(skip, u, ys[k])};
                     store_vec<1>(static_cast<T*>(p.dz) + at, o_z);
                 }
-                dD = fmaf(dyg[j], u[j], dD);
+                dD = fmaf(dys[k], u, dD);
                 dbias += o_dt[0];
             }
         }
@@ -289,7 +385,7 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
     __syncthreads();
     if (on) {
 #pragma unroll
-        for (int i = 0; i < kS; i++) {
+        for (int i = 0; i < kStates; i++) {
             if (n0 + i < p.N) {
                 p.part_c[((size_t)w.b * (p.N + 2) + n0 + i) * p.C + c] = dA[i];
                 if (p.dh0) p.dh0[((size_t)w.b * p.C + c) * p.N + n0 + i] = g[i];
@@ -353,35 +449,50 @@ Layout layout(int B, int T, int C, int N) {
     const size_t chunks = ((size_t)T + K - 1) / K, cblocks = ((size_t)C + 31) / 32;
     const auto up = [](size_t x) { return (x + 3) / 4 * 4; };
     Layout l{};
-    l.ckpt = up((size_t)B * chunks * kS * nw * C);
+    l.ckpt = up((size_t)B * chunks * kStates * nw * C);
     l.part_bc = up(cblocks * B * T * 2 * N);
     l.part_c = up((size_t)B * (N + 2) * C);
     l.total = l.ckpt + l.part_bc + l.part_c;
     return l;
 }
 
-template <typename T, int kNW>
+template <typename T, int kNW, bool kVecRows, bool kVecBC>
 cudaError_t launch(const SsmBwdParams& p, cudaStream_t stream) {
     constexpr int kK = chunk_for(kNW);
     const unsigned grid = (unsigned)((long long)p.B * p.cblocks);
-    ttt_ssm_checkpoint_kernel<T, kNW, kK><<<grid, 32 * kNW, 0, stream>>>(p);
-    cudaError_t e = cudaPeekAtLastError();
+    const auto first = ttt_ssm_checkpoint_kernel<T, kNW, kK, kVecRows, kVecBC>;
+    const auto second = ttt_ssm_backward_kernel<T, kNW, kK, kVecRows, kVecBC>;
+    constexpr int smem1 = (int)sizeof(CkptSmem<T, kNW, 2 * kK>), smem2 = (int)sizeof(BwdSmem<T, kNW, kK>);
+    static_assert(smem1 <= (int)kMaxSmem && smem2 <= (int)kMaxSmem, "fits an SM");
+    cudaError_t e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(second, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2);
     if (e != cudaSuccess) return e;
-    constexpr int smem = (int)sizeof(BwdSmem<kNW, kK>);
-    e = cudaFuncSetAttribute(ttt_ssm_backward_kernel<T, kNW, kK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    first<<<grid, 32 * kNW, smem1, stream>>>(p);
+    e = cudaPeekAtLastError();
     if (e != cudaSuccess) return e;
-    ttt_ssm_backward_kernel<T, kNW, kK><<<grid, 32 * kNW, smem, stream>>>(p);
+    second<<<grid, 32 * kNW, smem2, stream>>>(p);
     return cudaPeekAtLastError();
+}
+
+template <typename T, int kNW>
+cudaError_t by_alignment(const SsmBwdParams& p, cudaStream_t stream) {
+    constexpr int es = sizeof(T);
+    const bool rows = rows16(p.u, p.ld_u, p.C, es) && rows16(p.dt, p.ld_dt, p.C, es) && rows16(p.z, p.ld_z, p.C, es) &&
+                      rows16(p.dy, p.C, p.C, es);
+    const bool bc = rows16(p.Bm, p.ld_b, p.N, es) && rows16(p.Cm, p.ld_c, p.N, es);
+    if (rows && bc) return launch<T, kNW, true, true>(p, stream);
+    if (rows) return launch<T, kNW, true, false>(p, stream);
+    return launch<T, kNW, false, false>(p, stream);
 }
 
 template <typename T>
 cudaError_t dispatch(const SsmBwdParams& p, cudaStream_t stream) {
     switch (warps_for(p.N)) {
-        case 1: return launch<T, 1>(p, stream);
-        case 2: return launch<T, 2>(p, stream);
-        case 4: return launch<T, 4>(p, stream);
-        case 8: return launch<T, 8>(p, stream);
-        default: return launch<T, 16>(p, stream);
+        case 1: return by_alignment<T, 1>(p, stream);
+        case 2: return by_alignment<T, 2>(p, stream);
+        case 4: return by_alignment<T, 4>(p, stream);
+        case 8: return by_alignment<T, 8>(p, stream);
+        default: return by_alignment<T, 16>(p, stream);
     }
 }
 

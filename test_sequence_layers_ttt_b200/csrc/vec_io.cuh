@@ -82,7 +82,94 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
     }
 }
 
-// logistic function; 1 / (1 + e^-x) with e^-x = 0 or infinity at the ends gives 1 or 0
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// A row's V elements as they come from memory, to be unpacked when they are used
+template <typename T, int V>
+struct Raw {
+    static constexpr int kWords = V * (int)sizeof(T) / 4;  // 0: one bf16
+    uint32_t w[kWords > 0 ? kWords : 1];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (kWords == 0) {
+            w[0] = *reinterpret_cast<const unsigned short*>(p);
+        } else if constexpr (kWords == 1) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (kWords == 2) {
+            const uint2 r = *reinterpret_cast<const uint2*>(p);
+            w[0] = r.x;
+            w[1] = r.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 r = reinterpret_cast<const uint4*>(p)[i / 4];
+                w[i] = r.x;
+                w[i + 1] = r.y;
+                w[i + 2] = r.z;
+                w[i + 3] = r.w;
+            }
+        }
+    }
+    // elements [at, at + V) of a row of `width`: those before 0 or past the end are zeros and are not read
+    __device__ __forceinline__ void load_within(const T* row, int at, int width) {
+        if (at >= 0 && at + V <= width) {
+            load(row + at);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < (kWords > 0 ? kWords : 1); i++) w[i] = 0u;
+        if (at + V <= 0 || at >= width) return;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+            if (at + i < 0 || at + i >= width) continue;
+            if constexpr (sizeof(T) == 4)
+                w[i] = reinterpret_cast<const uint32_t*>(row)[at + i];
+            else
+                w[i / 2] |= (uint32_t) reinterpret_cast<const unsigned short*>(row)[at + i] << (i % 2 * 16);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; i++) v[i] = __uint_as_float(w[i]);
+        } else if constexpr (V == 1) {
+            v[0] = __uint_as_float(w[0] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i++) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+
+// Elements [at, at + V) of a row of `width` that lie in it
+template <int V, typename T>
+__device__ __forceinline__ void store_within(T* row, int at, int width, const float (&v)[V]) {
+    if (at >= 0 && at + V <= width) {
+        store_vec<V>(row + at, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++)
+        if (at + i >= 0 && at + i < width) {
+            const float one[1] = {v[i]};
+            store_vec<1>(row + at + i, one);
+        }
+}
+
+// 2^x and 1 / x by the special-function unit, tiny results flushed to zero (the forms that keep them cost
+// four instructions more)
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// logistic function 1 / (1 + e^-x); at the ends e^-x is 0 or infinity and the result 1 or 0
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-1.4426950408889634f * x)); }
 
 }  // namespace ttt
