@@ -39,26 +39,6 @@ __device__ __forceinline__ float softplus(float x) {
     return fmaf(s, p, fmaxf(x, 0.f));
 }
 
-// Two floats in one 64-bit register pair, for the packed fp32 instructions of sm_100.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 // 2^x in the place of `near_one` where |x| >= 1/16: one comparison and a predicated instruction
 __device__ __forceinline__ void ex2_beyond(float& near_one, float x) {
     asm("{\n .reg .pred p;\n .reg .f32 m;\n abs.f32 m, %1;\n setp.ge.f32 p, m, 0f3D800000;\n"

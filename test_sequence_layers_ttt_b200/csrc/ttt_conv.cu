@@ -14,6 +14,8 @@
 #include "block_internal.h"
 #include "vec_io.cuh"
 
+#include <type_traits>
+
 namespace ttt {
 namespace {
 
@@ -30,11 +32,10 @@ struct ConvParams {
     const float *weight, *bias;
     const int* lengths;
     void *y, *state_T;
-    int silu;
 };
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 8;  // rows on their way while the ones before them are worked on
+constexpr int kAhead = 4;  // rows on their way while the four before them are worked on
 
 // Row t of the window of sequence b (t < 0: the state's rows), the thread's channels.
 template <typename T, int V, int W>
@@ -49,8 +50,64 @@ __device__ __forceinline__ void window_row(const T* x, const T* state, long long
     }
 }
 
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) ttt_conv_kernel(const ConvParams p) {
+// The taps of V neighbouring channels: V W floats side by side
+template <int V, int W>
+__device__ __forceinline__ void load_taps(const float* weight, int c, f2 (&w)[W][(V + 1) / 2]) {
+    float v[V * W];
+    if constexpr (V * W % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V * W / 4; i++) {
+            const float4 r = reinterpret_cast<const float4*>(weight + (size_t)c * W)[i];
+            v[4 * i] = r.x;
+            v[4 * i + 1] = r.y;
+            v[4 * i + 2] = r.z;
+            v[4 * i + 3] = r.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; i++) v[i] = weight[(size_t)c * W + i];
+    }
+#pragma unroll
+    for (int j = 0; j < W; j++) {
+        float tap[V];
+#pragma unroll
+        for (int k = 0; k < V; k++) tap[k] = v[k * W + j];
+        to_pairs<V>(tap, w[j]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_bias(const float* bias, int c, f2 (&o)[(V + 1) / 2]) {
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; k++) v[k] = bias ? bias[c + k] : 0.f;
+    to_pairs<V>(v, o);
+}
+
+// bias + sum_j w_j x: the window's rows, then the newest
+template <int W, int P>
+__device__ __forceinline__ void taps(const f2 (&w)[W][P], const f2 (&bias)[P], const f2 (&win)[W - 1][P], const f2 (&in)[P],
+                                     f2 (&a)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; k++) {
+        a[k] = fma2(w[0][k], win[0][k], bias[k]);
+#pragma unroll
+        for (int j = 1; j < W - 1; j++) a[k] = fma2(w[j][k], win[j][k], a[k]);
+        a[k] = fma2(w[W - 1][k], in[k], a[k]);
+    }
+}
+template <int W, int P>
+__device__ __forceinline__ void shift_in(f2 (&win)[W - 1][P], const f2 (&in)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; k++) {
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; j++) win[j][k] = win[j + 1][k];
+        win[W - 2][k] = in[k];
+    }
+}
+
+template <typename T, int V, int W, bool kSilu>
+__global__ void __launch_bounds__(kThreads, 6) ttt_conv_kernel(const ConvParams p) {
+    constexpr int P = (V + 1) / 2;  // pairs
     const long long block = blockIdx.x;
     const int grp = (int)(block % p.groups);
     const int piece = (int)(block / p.groups % p.pieces);
@@ -62,18 +119,27 @@ __global__ void __launch_bounds__(kThreads) ttt_conv_kernel(const ConvParams p) 
     const T* state = p.state0 ? static_cast<const T*>(p.state0) + (long long)b * (W - 1) * p.C + c : nullptr;
     T* y = static_cast<T*>(p.y) + (long long)b * p.T * p.C + c;
 
-    float w[W][V], bias[V], win[W - 1][V];
-#pragma unroll
-    for (int k = 0; k < V; k++) {
-        bias[k] = p.bias ? p.bias[c + k] : 0.f;
-#pragma unroll
-        for (int j = 0; j < W; j++) w[j][k] = p.weight[(size_t)(c + k) * W + j];
-    }
     const int t0 = piece * p.piece, t1 = min(t0 + p.piece, p.T);
     const int live = min(t1, n);
+    // Two batches of rows: one on its way while the other is worked on.  (A batch is loaded as a whole: a
+    // load into a slot just used up would have to be waited for together with the oldest one.)
+    Raw<T, V> rows[2][kAhead];
+    const auto load = [&](Raw<T, V>(&to)[kAhead], int t) {
+#pragma unroll
+        for (int r = 0; r < kAhead; r++)
+            if (t + r < live) to[r].load(x + (long long)(t + r) * p.ld);
+    };
+    load(rows[0], t0);
+    f2 w[W][P], bias[P], win[W - 1][P];
+    load_bias<V>(p.bias, c, bias);
+    load_taps<V, W>(p.weight, c, w);
     if (t0 < live) {
 #pragma unroll
-        for (int i = 0; i < W - 1; i++) window_row<T, V, W>(x, state, p.ld, p.C, t0 - (W - 1) + i, win[i]);
+        for (int i = 0; i < W - 1; i++) {
+            float v[V];
+            window_row<T, V, W>(x, state, p.ld, p.C, t0 - (W - 1) + i, v);
+            to_pairs<V>(v, win[i]);
+        }
     }
     // The final state, by the threads of the first piece, who alone read state0: it may be written in
     // place.  They have what they need of it in `win` (t0 = 0) or read it here before they write.
@@ -85,32 +151,34 @@ __global__ void __launch_bounds__(kThreads) ttt_conv_kernel(const ConvParams p) 
 #pragma unroll
         for (int i = 0; i < W - 1; i++) store_vec<V>(out + (long long)i * p.C, last[i]);
     }
-    Raw<T, V> next[kAhead];
-#pragma unroll
-    for (int r = 0; r < kAhead; r++)
-        if (t0 + r < live) next[r].load(x + (long long)(t0 + r) * p.ld);
-    int t = t0;
-    for (; t < live; t += kAhead) {
+    const auto work = [&](const Raw<T, V>(&from)[kAhead], int t, auto whole) {
 #pragma unroll
         for (int r = 0; r < kAhead; r++) {
-            if (t + r < live) {
-                float in[V], o[V];
-                next[r].get(in);
-                if (t + kAhead + r < live) next[r].load(x + (long long)(t + kAhead + r) * p.ld);
+            if (!decltype(whole)::value && t + r >= live) break;
+            float v[V];
+            f2 in[P], a[P];
+            from[r].get(v);
+            to_pairs<V>(v, in);
+            taps<W, P>(w, bias, win, in, a);
+            shift_in<W, P>(win, in);
+            if constexpr (kSilu)
 #pragma unroll
-                for (int k = 0; k < V; k++) {
-                    float a = bias[k];
-#pragma unroll
-                    for (int j = 0; j < W - 1; j++) a += w[j][k] * win[j][k];
-                    a += w[W - 1][k] * in[k];
-#pragma unroll
-                    for (int j = 0; j + 1 < W - 1; j++) win[j][k] = win[j + 1][k];
-                    win[W - 2][k] = in[k];
-                    o[k] = p.silu ? a * sigmoid(a) : a;
-                }
-                store_vec<V>(y + (long long)(t + r) * p.C, o);
-            }
+                for (int k = 0; k < P; k++) a[k] = mul2(a[k], sigmoid2(a[k]));
+            from_pairs<V>(a, v);
+            store_vec<V>(y + (long long)(t + r) * p.C, v);
         }
+    };
+    int t = t0;
+    for (; t + 2 * kAhead <= live; t += 2 * kAhead) {
+        load(rows[1], t + kAhead);
+        work(rows[0], t, std::true_type{});
+        load(rows[0], t + 2 * kAhead);
+        work(rows[1], t + kAhead, std::true_type{});
+    }
+    if (t < live) {
+        load(rows[1], t + kAhead);
+        work(rows[0], t, std::false_type{});
+        work(rows[1], t + kAhead, std::false_type{});
     }
     float zero[V];
 #pragma unroll
@@ -126,162 +194,168 @@ struct ConvBwdParams {
     const int* lengths;
     void *dx, *dstate0;
     float* partial;  // [B][pieces][W + 1][C]
-    int silu;
 };
 
-constexpr int kBack = 4;  // rows of x and dy on their way
-constexpr int kLanes = 32, kSub = 4;  // threads: 32 channel vectors x 4 runs of a piece's tokens
+constexpr int kBack = 4;     // rows of x and dy on their way
+constexpr int kBackVec = 4;  // channels a thread, where rows allow it
 
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(kLanes * kSub) ttt_conv_backward_kernel(const ConvBwdParams p) {
-    __shared__ float s[kSub][W + 1][kLanes * V];
+template <typename T, int V, int W, bool kSilu>
+__global__ void __launch_bounds__(kThreads, 4) ttt_conv_backward_kernel(const ConvBwdParams p) {
+    constexpr int P = (V + 1) / 2;
     const long long block = blockIdx.x;
     const int grp = (int)(block % p.groups);
     const int piece = (int)(block / p.groups % p.pieces);
     const int b = (int)(block / p.groups / p.pieces);
-    const int c = (grp * kLanes + threadIdx.x) * V;
-    const bool on = c < p.C;
+    const int c = (grp * kThreads + threadIdx.x) * V;
+    if (c >= p.C) return;
     const int n = length_of(p.lengths, b, p.T);
 
-    float dw[W][V], db[V];
+    const f2 zero2 = pack2(0.f, 0.f), one2 = pack2(1.f, 1.f);
+    f2 dw[W][P], db[P];
 #pragma unroll
-    for (int k = 0; k < V; k++) {
-        db[k] = 0.f;
+    for (int k = 0; k < P; k++) {
+        db[k] = zero2;
 #pragma unroll
-        for (int j = 0; j < W; j++) dw[j][k] = 0.f;
+        for (int j = 0; j < W; j++) dw[j][k] = zero2;
     }
-    if (on) {
+    // This piece: the gradients of rows [r0, t1) of the window, which for the first piece begins W - 1 rows
+    // before token 0 (the state's rows).  Row t needs dp_t .. dp_{t + W - 1}; dp of the piece's own tokens
+    // counts for dw.
+    const int t0 = piece * p.piece, t1 = min(t0 + p.piece, p.T);
+    {
         const T* x = static_cast<const T*>(p.x) + (long long)b * p.T * p.ld + c;
         const T* state = p.state0 ? static_cast<const T*>(p.state0) + (long long)b * (W - 1) * p.C + c : nullptr;
         const T* dy = static_cast<const T*>(p.dy) + (long long)b * p.T * p.C + c;
         const T* dst = p.dstate_T ? static_cast<const T*>(p.dstate_T) + (long long)b * (W - 1) * p.C + c : nullptr;
         T* dx = static_cast<T*>(p.dx) + (long long)b * p.T * p.C + c;
         T* ds0 = p.dstate0 ? static_cast<T*>(p.dstate0) + (long long)b * (W - 1) * p.C + c : nullptr;
-        float w[W][V], bias[V], win[W - 1][V], dp[W - 1][V];
+        const int r0 = t0 == 0 ? -(W - 1) : t0, stop = t1 + W - 1, live = min(stop, n);
+        Raw<T, V> rows[2][kBack], grads[2][kBack];
+        const auto load = [&](int which, int t) {
 #pragma unroll
-        for (int k = 0; k < V; k++) {
-            bias[k] = p.bias ? p.bias[c + k] : 0.f;
-#pragma unroll
-            for (int j = 0; j < W; j++) w[j][k] = p.weight[(size_t)(c + k) * W + j];
-        }
-        // This run: the gradients of rows [r0, r1) of the window, which for the first run begins W - 1
-        // rows before token 0 (the state's rows).  Row t needs dp_t .. dp_{t + W - 1}; dp of the run's
-        // own tokens counts for dw.
-        const int run = p.piece / kSub;
-        const int t0 = piece * p.piece + (int)threadIdx.y * run, t1 = min(t0 + run, p.T);
-        const int r0 = t0 == 0 ? -(W - 1) : t0;
+            for (int q = 0; q < kBack; q++)
+                if (t + q < live) {
+                    rows[which][q].load(x + (long long)(t + q) * p.ld);
+                    grads[which][q].load(dy + (long long)(t + q) * p.C);
+                }
+        };
+        load(0, t0);
+        f2 w[W][P], bias[P], win[W - 1][P], dp[W - 1][P];
+        load_bias<V>(p.bias, c, bias);
+        load_taps<V, W>(p.weight, c, w);
 #pragma unroll
         for (int i = 0; i < W - 1; i++) {
 #pragma unroll
-            for (int k = 0; k < V; k++) dp[i][k] = win[i][k] = 0.f;
-            if (t0 < t1 && t0 < n) window_row<T, V, W>(x, state, p.ld, p.C, t0 - (W - 1) + i, win[i]);
+            for (int k = 0; k < P; k++) dp[i][k] = win[i][k] = zero2;
+            if (t0 < live) {
+                float v[V];
+                window_row<T, V, W>(x, state, p.ld, p.C, t0 - (W - 1) + i, v);
+                to_pairs<V>(v, win[i]);
+            }
         }
-        // step t: dp_t is computed, and with it row t - (W - 1) is complete
-        if (t0 < t1 || (t0 == 0 && p.T == 0)) {
-            const int stop = t1 + W - 1, live = min(stop, n);
-            Raw<T, V> next_x[kBack], next_g[kBack];
+        // Step t: dp_t is computed, and with it row t - (W - 1) is complete.  `inside`: both are tokens of the piece.
+        const auto step = [&](int t, const Raw<T, V>& row, const Raw<T, V>& grad, auto inside) {
+            constexpr bool kInside = decltype(inside)::value;
+            f2 now[P];
 #pragma unroll
-            for (int q = 0; q < kBack; q++)
-                if (t0 + q < live) {
-                    next_x[q].load(x + (long long)(t0 + q) * p.ld);
-                    next_g[q].load(dy + (long long)(t0 + q) * p.C);
-                }
-            for (int tq = t0; tq < stop; tq += kBack)
+            for (int k = 0; k < P; k++) now[k] = zero2;
+            if (kInside || t < live) {
+                float v[V];
+                f2 in[P], a[P];
+                row.get(v);
+                to_pairs<V>(v, in);
+                grad.get(v);
+                to_pairs<V>(v, now);
+                if constexpr (kSilu) {
+                    taps<W, P>(w, bias, win, in, a);
 #pragma unroll
-            for (int q = 0; q < kBack; q++) {
-                const int t = tq + q;
-                if (t >= stop) break;
-                float now[V];
-#pragma unroll
-                for (int k = 0; k < V; k++) now[k] = 0.f;
-                if (t < live) {
-                    float in[V], g[V];
-                    next_x[q].get(in);
-                    next_g[q].get(g);
-                    if (t + kBack < live) {
-                        next_x[q].load(x + (long long)(t + kBack) * p.ld);
-                        next_g[q].load(dy + (long long)(t + kBack) * p.C);
-                    }
-#pragma unroll
-                    for (int k = 0; k < V; k++) {
-                        float a = bias[k];
-#pragma unroll
-                        for (int j = 0; j < W - 1; j++) a += w[j][k] * win[j][k];
-                        a += w[W - 1][k] * in[k];
-                        const float sg = sigmoid(a);
-                        now[k] = p.silu ? g[k] * sg * (1.f + a * (1.f - sg)) : g[k];
-                        if (t < t1) {
-                            db[k] += now[k];
-#pragma unroll
-                            for (int j = 0; j < W - 1; j++) dw[j][k] += now[k] * win[j][k];
-                            dw[W - 1][k] += now[k] * in[k];
-                        }
-#pragma unroll
-                        for (int j = 0; j + 1 < W - 1; j++) win[j][k] = win[j + 1][k];
-                        win[W - 2][k] = in[k];
+                    for (int k = 0; k < P; k++) {  // dy s (1 + a (1 - s))
+                        const f2 sg = sigmoid2(a[k]);
+                        const f2 rest = fma2(sg, pack2(-1.f, -1.f), one2);
+                        now[k] = mul2(mul2(now[k], sg), fma2(a[k], rest, one2));
                     }
                 }
-                const int r = t - (W - 1);  // the row that is complete
-                if (r >= r0) {
-                    float o[V], add[V];
+                if (kInside || t < t1) {
 #pragma unroll
-                    for (int k = 0; k < V; k++) add[k] = 0.f;
-                    const int i = r + (W - 1) - n;  // its place in the final state
-                    if (dst && i >= 0 && i < W - 1) load_vec<V>(dst + (long long)i * p.C, add);
+                    for (int k = 0; k < P; k++) {
+                        db[k] = add2(db[k], now[k]);
 #pragma unroll
-                    for (int k = 0; k < V; k++) {
-                        float a = w[0][k] * now[k];
-#pragma unroll
-                        for (int j = 1; j < W; j++) a += w[j][k] * dp[W - 1 - j][k];
-                        o[k] = a + add[k];
+                        for (int j = 0; j < W - 1; j++) dw[j][k] = fma2(now[k], win[j][k], dw[j][k]);
+                        dw[W - 1][k] = fma2(now[k], in[k], dw[W - 1][k]);
                     }
-                    if (r >= 0)
-                        store_vec<V>(dx + (long long)r * p.C, o);
-                    else if (ds0)
-                        store_vec<V>(ds0 + (long long)(r + W - 1) * p.C, o);
                 }
+                shift_in<W, P>(win, in);
+            }
+            const int r = t - (W - 1);  // the row that is complete
+            f2 o2[P];
+            float o[V];
 #pragma unroll
-                for (int k = 0; k < V; k++) {
+            for (int k = 0; k < P; k++) {
+                o2[k] = mul2(w[0][k], now[k]);
 #pragma unroll
-                    for (int j = 0; j + 1 < W - 1; j++) dp[j][k] = dp[j + 1][k];
-                    dp[W - 2][k] = now[k];
+                for (int j = 1; j < W; j++) o2[k] = fma2(w[j][k], dp[W - 1 - j][k], o2[k]);
+            }
+            from_pairs<V>(o2, o);
+            if constexpr (kInside) {
+                store_vec<V>(dx + (long long)r * p.C, o);
+            } else if (r >= r0) {
+                const int i = t - n;  // its place in the final state
+                if (dst && i >= 0 && i < W - 1) {
+                    float add[V];
+                    load_vec<V>(dst + (long long)i * p.C, add);
+#pragma unroll
+                    for (int k = 0; k < V; k++) o[k] += add[k];
                 }
+                if (r >= 0)
+                    store_vec<V>(dx + (long long)r * p.C, o);
+                else if (ds0)
+                    store_vec<V>(ds0 + (long long)(r + W - 1) * p.C, o);
+            }
+            shift_in<W, P>(dp, now);
+        };
+        for (int tb = t0; tb < stop; tb += 2 * kBack) {
+            load(1, tb + kBack);
+            if (tb - (W - 1) >= t0 && tb + 2 * kBack <= min(t1, n)) {
+#pragma unroll
+                for (int q = 0; q < kBack; q++) step(tb + q, rows[0][q], grads[0][q], std::true_type{});
+                load(0, tb + 2 * kBack);
+#pragma unroll
+                for (int q = 0; q < kBack; q++) step(tb + kBack + q, rows[1][q], grads[1][q], std::true_type{});
+            } else {
+#pragma unroll
+                for (int q = 0; q < kBack; q++)
+                    if (tb + q < stop) step(tb + q, rows[0][q], grads[0][q], std::false_type{});
+                load(0, tb + 2 * kBack);
+#pragma unroll
+                for (int q = 0; q < kBack; q++)
+                    if (tb + kBack + q < stop) step(tb + kBack + q, rows[1][q], grads[1][q], std::false_type{});
             }
         }
     }
+    float* part = p.partial + (((size_t)b * p.pieces + piece) * (W + 1)) * p.C + c;
 #pragma unroll
-    for (int k = 0; k < V; k++) {
-#pragma unroll
-        for (int j = 0; j < W; j++) s[threadIdx.y][j][threadIdx.x * V + k] = dw[j][k];
-        s[threadIdx.y][W][threadIdx.x * V + k] = db[k];
-    }
-    __syncthreads();
-    for (int i = threadIdx.y * kLanes + threadIdx.x; i < (W + 1) * kLanes * V; i += kLanes * kSub) {
-        const int j = i / (kLanes * V), q = i % (kLanes * V);
-        const int ch = grp * kLanes * V + q;
-        if (ch < p.C) {
-            float a = s[0][j][q];
-#pragma unroll
-            for (int u = 1; u < kSub; u++) a += s[u][j][q];
-            p.partial[(((size_t)b * p.pieces + piece) * (W + 1) + j) * p.C + ch] = a;
-        }
+    for (int j = 0; j <= W; j++) {
+        float v[V];
+        from_pairs<V>(j < W ? dw[j % W] : db, v);
+        store_vec<V>(part + (size_t)j * p.C, v);
     }
 }
 
 // dweight [C][W] and dbias [C] from the pieces' partials [rows][W + 1][C]: 32 channels and one tap a
-// block, 8 threads a sum.  The order of the additions goes by the shape alone.
-__global__ void __launch_bounds__(256) ttt_conv_weight_sum_kernel(int rows, int W, int C, const float* __restrict__ partial,
-                                                                  float* __restrict__ dweight, float* __restrict__ dbias) {
-    __shared__ float s[8][33];
+// block, 32 threads a sum.  The order of the additions goes by the shape alone.
+__global__ void __launch_bounds__(1024) ttt_conv_weight_sum_kernel(int rows, int W, int C, const float* __restrict__ partial,
+                                                                   float* __restrict__ dweight, float* __restrict__ dbias) {
+    __shared__ float s[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y;
     float a = 0.f;
     if (c < C)
-        for (int r = threadIdx.y; r < rows; r += 8) a += partial[((size_t)r * (W + 1) + j) * C + c];
+#pragma unroll 4
+        for (int r = threadIdx.y; r < rows; r += 32) a += partial[((size_t)r * (W + 1) + j) * C + c];
     s[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
     if (threadIdx.y == 0 && c < C) {
 #pragma unroll
-        for (int i = 1; i < 8; i++) a += s[i][threadIdx.x];
+        for (int i = 1; i < 32; i++) a += s[i][threadIdx.x];
         if (j < W)
             dweight[(size_t)c * W + j] = a;
         else if (dbias)
@@ -294,11 +368,17 @@ bool rows_aligned(const void* p, long long ld, int bytes, int es) {
 }
 
 template <typename F>
-cudaError_t by_width(int W, F f) {
+cudaError_t by_width(int W, int silu, F f) {
+    const auto with = [&](auto w) {
+        if (silu)
+            f(w, std::true_type{});
+        else
+            f(w, std::false_type{});
+    };
     switch (W) {
-        case 2: f(std::integral_constant<int, 2>{}); break;
-        case 3: f(std::integral_constant<int, 3>{}); break;
-        case 4: f(std::integral_constant<int, 4>{}); break;
+        case 2: with(std::integral_constant<int, 2>{}); break;
+        case 3: with(std::integral_constant<int, 3>{}); break;
+        case 4: with(std::integral_constant<int, 4>{}); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaPeekAtLastError();
@@ -332,30 +412,31 @@ cudaError_t forward(const ConvArgs& a, cudaStream_t stream) {
     p.lengths = a.lengths;
     p.y = a.y;
     p.state_T = a.state_T;
-    p.silu = a.silu;
     const long long blocks = (long long)a.B * p.pieces * p.groups;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
-    return by_width(a.W, [&](auto w) {
+    return by_width(a.W, a.silu, [&](auto w, auto silu) {
         constexpr int W = decltype(w)::value;
+        constexpr bool kSilu = decltype(silu)::value;
         if (vec)
-            ttt_conv_kernel<T, kV, W><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+            ttt_conv_kernel<T, kV, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
         else
-            ttt_conv_kernel<T, 1, W><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+            ttt_conv_kernel<T, 1, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
     });
 }
 
-// Tokens a block of the backward takes: 512, halved down to 16 while the launch has fewer threads than
-// half of what 148 SMs hold.
+// Tokens a thread of the backward walks: 128, halved down to 16 while the launch has fewer than 256 threads for
+// each of 148 SMs.  The width of a block counts for DRAM: 128 threads side by side read 1 KB of a row, where 32
+// with their four warps at four places of the sequence took 1.4 times as long.
 int backward_piece(int B, int T, int C, int vec) {
-    const long long columns = (long long)B * ((C + kLanes * vec - 1) / (kLanes * vec)) * kLanes * kSub;
-    int piece = 512;
-    while (piece > 16 && columns * ((T + piece - 1) / piece) < 148LL * 1024) piece /= 2;
+    const long long columns = (long long)B * ((C + vec - 1) / vec);
+    int piece = 128;
+    while (piece > 16 && columns * ((T + piece - 1) / piece) < 148LL * 256) piece /= 2;
     return piece;
 }
 
 template <typename T>
 cudaError_t backward(const ConvBwdArgs& a, float* workspace, cudaStream_t stream) {
-    constexpr int kV = 4;
+    constexpr int kV = kBackVec;
     const bool vec = a.f.C % kV == 0 && rows_aligned(a.f.x, a.f.ld, kV * sizeof(T), sizeof(T));
     const int v = vec ? kV : 1;
     ConvBwdParams p{};
@@ -363,7 +444,7 @@ cudaError_t backward(const ConvBwdArgs& a, float* workspace, cudaStream_t stream
     p.C = a.f.C;
     p.piece = backward_piece(a.f.B, a.f.T, a.f.C, v);
     p.pieces = a.f.T > 0 ? (a.f.T + p.piece - 1) / p.piece : 1;
-    p.groups = (a.f.C + kLanes * v - 1) / (kLanes * v);
+    p.groups = (a.f.C + kThreads * v - 1) / (kThreads * v);
     p.ld = a.f.ld;
     p.x = a.f.x;
     p.state0 = a.f.state0;
@@ -375,18 +456,18 @@ cudaError_t backward(const ConvBwdArgs& a, float* workspace, cudaStream_t stream
     p.dx = a.dx;
     p.dstate0 = a.dstate0;
     p.partial = workspace;
-    p.silu = a.f.silu;
     const long long blocks = (long long)a.f.B * p.pieces * p.groups;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
-    cudaError_t e = by_width(a.f.W, [&](auto w) {
+    cudaError_t e = by_width(a.f.W, a.f.silu, [&](auto w, auto silu) {
         constexpr int W = decltype(w)::value;
+        constexpr bool kSilu = decltype(silu)::value;
         if (vec)
-            ttt_conv_backward_kernel<T, kV, W><<<(unsigned)blocks, dim3(kLanes, kSub), 0, stream>>>(p);
+            ttt_conv_backward_kernel<T, kV, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
         else
-            ttt_conv_backward_kernel<T, 1, W><<<(unsigned)blocks, dim3(kLanes, kSub), 0, stream>>>(p);
+            ttt_conv_backward_kernel<T, 1, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
     });
     if (e != cudaSuccess) return e;
-    ttt_conv_weight_sum_kernel<<<dim3((a.f.C + 31) / 32, a.f.W + 1), dim3(32, 8), 0, stream>>>(
+    ttt_conv_weight_sum_kernel<<<dim3((a.f.C + 31) / 32, a.f.W + 1), dim3(32, 32), 0, stream>>>(
         a.f.B * p.pieces, a.f.W, a.f.C, workspace, a.dweight, a.dbias);
     return cudaPeekAtLastError();
 }
@@ -401,7 +482,7 @@ size_t conv_backward_workspace_bytes(int B, int T, int C, int W) {
     if (B < 1 || T < 0 || C < 1 || W < 2 || W > kConvMaxWidth) return 0;
     // the launch picks four channels a thread, or one where alignment asks for it: room for either
     size_t most = 0;
-    for (int v : {1, 4}) {
+    for (int v : {1, kBackVec}) {
         const int piece = backward_piece(B, T, C, v);
         const size_t pieces = T > 0 ? (T + piece - 1) / piece : 1;
         const size_t bytes = (size_t)B * pieces * (W + 1) * C * sizeof(float);

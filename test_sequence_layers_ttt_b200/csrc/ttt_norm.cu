@@ -7,18 +7,22 @@
 //     dh_j = r (v_j - h_j r^2 mean_i(v_i h_i)) + g_j,    dw_j = sum over rows of dy_j h_j r
 //
 // Both are bound by HBM: every element is read once and written once, kept in registers between.  A row
-// belongs to one group of threads (a warp, or a block of 64 to 1024), each holding kNV vectors of 16
-// bytes; a group walks rows with a stride, the next row on its way while one is worked on, and keeps its
-// part of the weight.  The sum of squares and the largest |h w| (y / scale is h w 448 / max |h w|, without r)
-// meet in one reduction, so 8 bits cost no second one.  Sums are in fp32; y, h, dh are rounded once.
+// belongs to one group of threads (a part of a warp, a warp, or a block of up to 512), each holding kNV vectors of 16 bytes,
+// 16 elements where the row is long enough: with 8 the reduction, some 70 instructions a thread and row, took
+// as many as the elements.  A group walks rows with a stride and keeps its part of the weight; in the forward
+// the next row is on its way while one is worked on, in the backward, whose registers are full, other blocks of
+// the SM have theirs.  The sum of squares and the largest |h w| (y / scale is h w 448 / max |h w|,
+// without r) meet in one reduction, so 8 bits cost no second one.  Sums are in fp32; y, h, dh are rounded once.
 //
-// Where d is no multiple of a vector, rows start inside one: a group counts its vectors from the 16-byte
-// boundary before its row, and the two at the ends go element by element.  The stride is a multiple of 8
-// rows, so that all rows of a group start at the same place in a vector.
+// Where d is no multiple of a vector (kShift), rows start inside one: a group counts its vectors from the
+// 16-byte boundary before its row, and the two at the ends go element by element.  The stride is a multiple of
+// 8 rows, so that all rows of a group start at the same place in a vector.
 #include <cuda_fp8.h>
 
 #include "block_internal.h"
 #include "vec_io.cuh"
+
+#include <type_traits>
 
 namespace ttt {
 namespace {
@@ -32,15 +36,14 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
     return make_float2(a.x + b.x, kMax ? fmaxf(a.y, b.y) : a.y + b.y);
 }
 
-// blockDim.x threads a row; blockDim.y > 1 only with blockDim.x = 32.  `s` is free again after the
-// next __syncthreads, which a caller that reduces once per row of a loop gets from the double buffer.
+// blockDim.x threads a row: a power of two up to a warp, or whole warps.  `s` is free again after the next
+// __syncthreads, which a caller that reduces once per row of a loop gets from the double buffer.
 template <bool kMax>
 __device__ __forceinline__ float2 reduce_row(float2 v, float2* s) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = min((int)blockDim.x, 32) / 2; o > 0; o >>= 1)
         v = join<kMax>(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
+    if (warps <= 1) return v;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
     v = s[0];
@@ -59,6 +62,26 @@ template <int V>
 __device__ __forceinline__ int place(int i, int off) {
     return (int)(threadIdx.x + i * blockDim.x) * V - off;
 }
+template <bool kShift, typename T, int V>
+__device__ __forceinline__ void load_at(Raw<T, V>& r, const T* row, int at, int d) {
+    if constexpr (kShift) {
+        r.load_within(row, at, d);
+    } else if (at < d) {
+        r.load(row + at);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Raw<T, V>::kWords; i++) r.w[i] = 0u;
+    }
+}
+template <bool kShift, int V, typename T>
+__device__ __forceinline__ void store_at(T* row, int at, int d, const f2 (&o)[V / 2]) {
+    float v[V];
+    from_pairs<V>(o, v);
+    if constexpr (kShift)
+        store_within<V>(row, at, d, v);
+    else
+        store_vec<V>(row + at, v);
+}
 
 struct NormParams {
     long long rows;
@@ -70,55 +93,78 @@ struct NormParams {
     float* scale;  // 8 bits only
 };
 
-// A thread with one vector has room in 64 registers, so a row may have 1024 of them; with more vectors 512
-constexpr int most_threads(int nv) { return nv == 1 ? 1024 : 512; }
-
-template <typename T, int kNV, bool kQ8>
-__global__ void __launch_bounds__(most_threads(kNV)) ttt_rmsnorm_kernel(const NormParams p) {
-    constexpr int V = Elem<T>::kVec;
-    __shared__ float2 s[2][32];
+template <typename T, int kNV, bool kShift, bool kQ8>
+__global__ void __launch_bounds__(512) ttt_rmsnorm_kernel(const NormParams p) {
+    constexpr int V = Elem<T>::kVec, P = V / 2;
+    __shared__ float2 s[2][16];
     const long long group = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const long long groups = (long long)gridDim.x * blockDim.y;
-    if (group >= p.rows) return;  // whole warps only: blockDim.y > 1 means one warp a row
-    const int off = (int)((size_t)group * p.d % V);
-    const T* const x = static_cast<const T*>(p.x);
-    const T* const res = static_cast<const T*>(p.residual);
+    const int off = kShift ? (int)((size_t)group * p.d % V) : 0;
+    const T* x = static_cast<const T*>(p.x) + (size_t)group * p.d;
+    const T* res = p.residual ? static_cast<const T*>(p.residual) + (size_t)group * p.d : nullptr;
+    const size_t stride = (size_t)groups * p.d;
     Raw<T, V> nx[kNV], nr[kNV];
-    float w[kNV][V];
+    f2 w[kNV][P];
+#pragma unroll
+    for (int i = 0; i < kNV; i++) {
+        const int at = place<V>(i, off), d = group < p.rows ? p.d : -V;
+        load_at<kShift>(nx[i], x, at, d);
+        if (res) load_at<kShift>(nr[i], res, at, d);
+    }
 #pragma unroll
     for (int i = 0; i < kNV; i++) {
         const int at = place<V>(i, off);
-        nx[i].load_within(x + (size_t)group * p.d, at, p.d);
-        if (res) nr[i].load_within(res + (size_t)group * p.d, at, p.d);
+        float v[V];
 #pragma unroll
-        for (int k = 0; k < V; k++) w[i][k] = at + k >= 0 && at + k < p.d ? p.weight[at + k] : 0.f;
+        for (int k = 0; k < V; k++) v[k] = at + k >= 0 && at + k < p.d ? p.weight[at + k] : 0.f;
+        to_pairs<V>(v, w[i]);
     }
     int buf = 0;
-    for (long long row = group; row < p.rows; row += groups, buf ^= 1) {
+    // all rows of a block go round together; one past the end has zeros and writes nothing
+    for (long long row = group; row - threadIdx.y < p.rows; row += groups, buf ^= 1) {
         const size_t base = (size_t)row * p.d;
-        float h[kNV][V];
-        float2 acc = make_float2(0.f, 0.f);
+        const int d = row < p.rows ? p.d : -V;
+        f2 h[kNV][P], sq = pack2(0.f, 0.f);
+        float most = 0.f;
 #pragma unroll
         for (int i = 0; i < kNV; i++) {
-            nx[i].get(h[i]);
+            pairs_of(nx[i], h[i]);
             if (res) {
-                float r[V];
-                nr[i].get(r);
+                f2 r[P];
+                pairs_of(nr[i], r);
 #pragma unroll
-                for (int k = 0; k < V; k++) h[i][k] += r[k];
-            }
-            if (row + groups < p.rows) {
-                const int at = place<V>(i, off);
-                nx[i].load_within(x + base + (size_t)groups * p.d, at, p.d);
-                if (res) nr[i].load_within(res + base + (size_t)groups * p.d, at, p.d);
-            }
-#pragma unroll
-            for (int k = 0; k < V; k++) {
-                acc.x += h[i][k] * h[i][k];
-                if (kQ8) acc.y = fmaxf(acc.y, fabsf(h[i][k] * w[i][k]));
+                for (int k = 0; k < P; k++) h[i][k] = add2(h[i][k], r[k]);
             }
         }
-        acc = reduce_row<true>(acc, s[buf]);
+        x += stride;
+        if (res) res += stride;
+        if (row - threadIdx.y + groups < p.rows) {
+            const int next = row + groups < p.rows ? p.d : -V;
+#pragma unroll
+            for (int i = 0; i < kNV; i++) {
+                const int at = place<V>(i, off);
+                load_at<kShift>(nx[i], x, at, next);
+                if (res) load_at<kShift>(nr[i], res, at, next);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kNV; i++) {
+            const int at = place<V>(i, off);
+            if (p.h && at < d && at + V > 0) store_at<kShift, V>(static_cast<T*>(p.h) + base, at, d, h[i]);
+#pragma unroll
+            for (int k = 0; k < P; k++) {
+                sq = fma2(h[i][k], h[i][k], sq);
+                h[i][k] = mul2(h[i][k], w[i][k]);
+                if constexpr (kQ8) {
+                    float lo, hi;
+                    unpack2(h[i][k], lo, hi);
+                    most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+                }
+            }
+        }
+        float lo, hi;
+        unpack2(sq, lo, hi);
+        const float2 acc = reduce_row<true>(make_float2(lo + hi, most), s[buf]);
         const float r = rsqrtf(acc.x / (float)p.d + p.eps);
         float factor = r;  // y, or y / scale, is (h w) factor
         if (kQ8) {
@@ -130,21 +176,22 @@ __global__ void __launch_bounds__(most_threads(kNV)) ttt_rmsnorm_kernel(const No
                 scale = kScaleMin;
                 factor = fminf(r * (1.f / kScaleMin), 3e38f);
             }
-            if (threadIdx.x == 0) p.scale[row] = scale;
+            if (threadIdx.x == 0 && row < p.rows) p.scale[row] = scale;
         }
+        const f2 f = pack2(factor, factor);
 #pragma unroll
         for (int i = 0; i < kNV; i++) {
             const int at = place<V>(i, off);
-            if (at + V <= 0 || at >= p.d) continue;
-            if (p.h) store_within<V>(static_cast<T*>(p.h) + base, at, p.d, h[i]);
-            float y[V];
+            if (at >= d || at + V <= 0) continue;
 #pragma unroll
-            for (int k = 0; k < V; k++) y[k] = h[i][k] * w[i][k] * factor;
+            for (int k = 0; k < P; k++) h[i][k] = mul2(h[i][k], f);
             if constexpr (!kQ8) {
-                store_within<V>(static_cast<T*>(p.y) + base, at, p.d, y);
+                store_at<kShift, V>(static_cast<T*>(p.y) + base, at, p.d, h[i]);
             } else {
                 unsigned char* q = static_cast<unsigned char*>(p.y) + base;
-                if (at >= 0 && at + V <= p.d) {
+                float y[V];
+                from_pairs<V>(h[i], y);
+                if (!kShift || (at >= 0 && at + V <= p.d)) {
                     if constexpr (V == 8)
                         *reinterpret_cast<uint2*>(q + at) =
                             make_uint2(pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7]));
@@ -167,82 +214,102 @@ struct NormBwdParams {
     const void *h, *dy, *dh_in;
     const float* weight;
     void* dh;
-    float* partial;  // [groups][d]: each group's sum over its rows of dy h r
+    float* partial;  // [blocks][d]: each block's sum over its rows of dy h r
 };
 
-template <typename T, int kNV>
+template <typename T, int kNV, bool kShift>
 __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwdParams p) {
-    constexpr int V = Elem<T>::kVec;
-    __shared__ float2 s[2][32];
+    constexpr int V = Elem<T>::kVec, P = V / 2;
+    __shared__ float2 s[2][16];
     const long long group = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const long long groups = (long long)gridDim.x * blockDim.y;
-    const int off = (int)((size_t)group * p.d % V);
-    const T* const hp = static_cast<const T*>(p.h);
-    const T* const gp = static_cast<const T*>(p.dy);
-    const T* const ip = static_cast<const T*>(p.dh_in);
-    Raw<T, V> nh[kNV], ng[kNV], ni[kNV];
-    float w[kNV][V], dw[kNV][V];
+    const int off = kShift ? (int)((size_t)group * p.d % V) : 0;
+    const T* hp = static_cast<const T*>(p.h) + (size_t)group * p.d;
+    const T* gp = static_cast<const T*>(p.dy) + (size_t)group * p.d;
+    const T* ip = p.dh_in ? static_cast<const T*>(p.dh_in) + (size_t)group * p.d : nullptr;
+    const size_t stride = (size_t)groups * p.d;
+    f2 w[kNV][P], dw[kNV][P];
 #pragma unroll
     for (int i = 0; i < kNV; i++) {
         const int at = place<V>(i, off);
-        if (group < p.rows) {
-            nh[i].load_within(hp + (size_t)group * p.d, at, p.d);
-            ng[i].load_within(gp + (size_t)group * p.d, at, p.d);
-            if (ip) ni[i].load_within(ip + (size_t)group * p.d, at, p.d);
-        }
+        float v[V];
 #pragma unroll
-        for (int k = 0; k < V; k++) {
-            dw[i][k] = 0.f;
-            w[i][k] = at + k >= 0 && at + k < p.d ? p.weight[at + k] : 0.f;
-        }
+        for (int k = 0; k < V; k++) v[k] = at + k >= 0 && at + k < p.d ? p.weight[at + k] : 0.f;
+        to_pairs<V>(v, w[i]);
+#pragma unroll
+        for (int k = 0; k < P; k++) dw[i][k] = pack2(0.f, 0.f);
     }
     int buf = 0;
-    for (long long row = group; row < p.rows; row += groups, buf ^= 1) {
-        const size_t base = (size_t)row * p.d, next = base + (size_t)groups * p.d;
-        const bool more = row + groups < p.rows;
-        float h[kNV][V], dy[kNV][V];
-        float2 acc = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kNV; i++) {
-            nh[i].get(h[i]);
-            ng[i].get(dy[i]);
-            if (more) {
-                const int at = place<V>(i, off);
-                nh[i].load_within(hp + next, at, p.d);
-                ng[i].load_within(gp + next, at, p.d);
-            }
-#pragma unroll
-            for (int k = 0; k < V; k++) {
-                acc.x += h[i][k] * h[i][k];
-                acc.y += dy[i][k] * w[i][k] * h[i][k];
-            }
-        }
-        acc = reduce_row<false>(acc, s[buf]);
-        const float r = rsqrtf(acc.x / (float)p.d + p.eps);
-        const float c = r * r * (acc.y / (float)p.d);
+    for (long long row = group; row - threadIdx.y < p.rows; row += groups, buf ^= 1) {
+        const int d = row < p.rows ? p.d : -V;
+        f2 h[kNV][P], dy[kNV][P], sq = pack2(0.f, 0.f), dot = sq;
+        Raw<T, V> rh[kNV], rg[kNV], past[kNV];
 #pragma unroll
         for (int i = 0; i < kNV; i++) {
             const int at = place<V>(i, off);
-            if (at + V <= 0 || at >= p.d) continue;
-            float o[V], g[V];
-            if (ip) {
-                ni[i].get(g);
-                if (more) ni[i].load_within(ip + next, at, p.d);
-            }
+            load_at<kShift>(rh[i], hp, at, d);
+            load_at<kShift>(rg[i], gp, at, d);
+            if (ip) load_at<kShift>(past[i], ip, at, d);
+        }
+        hp += stride;
+        gp += stride;
+        if (ip) ip += stride;
 #pragma unroll
-            for (int k = 0; k < V; k++) {
-                o[k] = r * (dy[i][k] * w[i][k] - h[i][k] * c) + (ip ? g[k] : 0.f);
-                dw[i][k] += dy[i][k] * (h[i][k] * r);
+        for (int i = 0; i < kNV; i++) {
+            pairs_of(rh[i], h[i]);
+            pairs_of(rg[i], dy[i]);
+#pragma unroll
+            for (int k = 0; k < P; k++) {
+                sq = fma2(h[i][k], h[i][k], sq);
+                dot = fma2(mul2(dy[i][k], w[i][k]), h[i][k], dot);
             }
-            store_within<V>(static_cast<T*>(p.dh) + base, at, p.d, o);
+        }
+        float a0, a1, b0, b1;
+        unpack2(sq, a0, a1);
+        unpack2(dot, b0, b1);
+        const float2 acc = reduce_row<false>(make_float2(a0 + a1, b0 + b1), s[buf]);
+        const float r = rsqrtf(acc.x / (float)p.d + p.eps);
+        const float c = -r * r * r * (acc.y / (float)p.d);
+        const f2 r2 = pack2(r, r), c2 = pack2(c, c);
+        T* out = static_cast<T*>(p.dh) + (size_t)row * p.d;
+#pragma unroll
+        for (int i = 0; i < kNV; i++) {
+            const int at = place<V>(i, off);
+            f2 o[P];
+            if (ip)
+                pairs_of(past[i], o);
+            else
+#pragma unroll
+                for (int k = 0; k < P; k++) o[k] = pack2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < P; k++) {
+                o[k] = fma2(c2, h[i][k], o[k]);
+                const f2 rdy = mul2(r2, dy[i][k]);
+                o[k] = fma2(rdy, w[i][k], o[k]);
+                dw[i][k] = fma2(rdy, h[i][k], dw[i][k]);
+            }
+            if (at < d && at + V > 0) store_at<kShift, V>(out, at, d, o);
         }
     }
+    // rows of a block that are side by side (d at most 16 elements of 32 lanes) are added up first
+    __shared__ float sums[128 * 16];
+    float* part = blockDim.y > 1 ? sums + threadIdx.y * p.d : p.partial + (size_t)blockIdx.x * p.d;
 #pragma unroll
     for (int i = 0; i < kNV; i++) {
         const int at = place<V>(i, off);
+        float v[V];
+        from_pairs<V>(dw[i], v);
 #pragma unroll
         for (int k = 0; k < V; k++)
-            if (at + k >= 0 && at + k < p.d) p.partial[(size_t)group * p.d + at + k] = dw[i][k];
+            if (at + k >= 0 && at + k < p.d) part[at + k] = v[k];
+    }
+    if (blockDim.y > 1) {
+        __syncthreads();
+        for (int j = threadIdx.y * blockDim.x + threadIdx.x; j < p.d; j += blockDim.x * blockDim.y) {
+            float a = 0.f;
+            for (int y = 0; y < (int)blockDim.y; y++) a += sums[y * p.d + j];
+            p.partial[(size_t)blockIdx.x * p.d + j] = a;
+        }
     }
 }
 
@@ -251,51 +318,54 @@ struct Shape {
     long long blocks;
 };
 
-// Threads a row: the fewest that hold it in one vector each, from a warp up to `most`; past that 512 with
-// more vectors.  One warp a row packs four rows to a block.  Blocks: `resident` threads on each of 148 SMs
-// (1024 with 64 registers a thread, 768 with 80), or as many as there are rows; where rows start inside a
-// vector, rounded down to a multiple of 8.
-Shape shape_of(long long rows, int d, int es, int most, int resident) {
-    const int v = 16 / es, vecs = d % v == 0 ? d / v : (d + 2 * v - 2) / v;
-    Shape s{32, 4, 1, 0};
-    if (vecs > 32) {
-        s.threads_y = 1;
-        s.nv = vecs <= most ? 1 : (vecs + 511) / 512;
+// Threads a row: those that hold it in `nv` vectors each, nv = 16 elements (one vector where a warp or a part
+// of one then holds the row, twice as many where 512 threads would not).  Rows of a warp or less share a block of
+// 128 threads.  Blocks: `resident` threads on each of 148 SMs, or as many as there are rows; where rows start
+// inside a vector, rounded down to a multiple of 8.
+Shape shape_of(long long rows, int d, int es, int resident) {
+    const int v = 16 / es, vecs = d % v == 0 ? d / v : (d + 2 * v - 2) / v, usual = 16 / v;
+    Shape s{1, 1, 1, 0};
+    if (vecs <= 32) {
+        while (s.threads_x < vecs) s.threads_x *= 2;
+    } else {
+        s.nv = vecs <= 512 * usual ? usual : (vecs <= 1024 * usual ? 2 * usual : 2 * usual + 1);
         s.threads_x = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
     }
+    if (s.threads_x <= 32) s.threads_y = 128 / s.threads_x;
     const int a_block = s.threads_x * s.threads_y;
     s.blocks = 148LL * (a_block < resident ? resident / a_block : 1);
     if (d % v != 0) s.blocks -= s.blocks % 8;
     const long long need = (rows + s.threads_y - 1) / s.threads_y;
-    if (s.blocks > need) s.blocks = need;  // one row a group at most
+    if (s.blocks > need) s.blocks = need;  // a group then has one row at most
     return s;
 }
-Shape forward_shape(long long rows, int d, int es) { return shape_of(rows, d, es, 1024, 1024); }
-Shape backward_shape(long long rows, int d, int es) { return shape_of(rows, d, es, 512, 768); }
+Shape forward_shape(long long rows, int d, int es) { return shape_of(rows, d, es, 1024); }
+Shape backward_shape(long long rows, int d, int es) { return shape_of(rows, d, es, 512); }
 
-template <typename F>
-cudaError_t by_vectors(int nv, F f) {
-    switch (nv) {
-        case 1: f(std::integral_constant<int, 1>{}); break;
-        case 2: f(std::integral_constant<int, 2>{}); break;
-        case 3: f(std::integral_constant<int, 3>{}); break;
-        case 4: f(std::integral_constant<int, 4>{}); break;
-        case 5: f(std::integral_constant<int, 5>{}); break;
-        case 6: f(std::integral_constant<int, 6>{}); break;
-        case 7: f(std::integral_constant<int, 7>{}); break;
-        case 8: f(std::integral_constant<int, 8>{}); break;
-        case 9: f(std::integral_constant<int, 9>{}); break;
-        default: return cudaErrorInvalidValue;
-    }
-    return cudaPeekAtLastError();
+// f(vectors a thread, whether rows start inside a vector)
+template <typename T, typename F>
+cudaError_t by_vectors(int nv, int d, F f) {
+    constexpr int kV = Elem<T>::kVec, kUsual = 16 / kV;
+    const auto with = [&](auto n) {
+        if (d % kV)
+            f(n, std::true_type{});
+        else
+            f(n, std::false_type{});
+        return cudaPeekAtLastError();
+    };
+    if (nv == 1) return with(std::integral_constant<int, 1>{});
+    if (nv == kUsual) return with(std::integral_constant<int, kUsual>{});
+    if (nv == 2 * kUsual) return with(std::integral_constant<int, 2 * kUsual>{});
+    if (nv == 2 * kUsual + 1) return with(std::integral_constant<int, 2 * kUsual + 1>{});
+    return cudaErrorInvalidValue;
 }
 
 template <typename T, bool kQ8>
 cudaError_t launch_forward(const NormParams& p, cudaStream_t stream) {
     const Shape s = forward_shape(p.rows, p.d, sizeof(T));
     const dim3 block(s.threads_x, s.threads_y);
-    return by_vectors(s.nv, [&](auto nv) {
-        ttt_rmsnorm_kernel<T, decltype(nv)::value, kQ8><<<(unsigned)s.blocks, block, 0, stream>>>(p);
+    return by_vectors<T>(s.nv, p.d, [&](auto nv, auto shift) {
+        ttt_rmsnorm_kernel<T, decltype(nv)::value, decltype(shift)::value, kQ8><<<(unsigned)s.blocks, block, 0, stream>>>(p);
     });
 }
 
@@ -321,11 +391,11 @@ template <typename T>
 cudaError_t launch_backward(const NormBwdParams& p, float* dweight, cudaStream_t stream) {
     const Shape s = backward_shape(p.rows, p.d, sizeof(T));
     const dim3 block(s.threads_x, s.threads_y);
-    cudaError_t e = by_vectors(s.nv, [&](auto nv) {
-        ttt_rmsnorm_backward_kernel<T, decltype(nv)::value><<<(unsigned)s.blocks, block, 0, stream>>>(p);
+    cudaError_t e = by_vectors<T>(s.nv, p.d, [&](auto nv, auto shift) {
+        ttt_rmsnorm_backward_kernel<T, decltype(nv)::value, decltype(shift)::value><<<(unsigned)s.blocks, block, 0, stream>>>(p);
     });
     if (e != cudaSuccess) return e;
-    return launch_column_sum((int)(s.blocks * s.threads_y), p.d, p.partial, dweight, stream);
+    return launch_column_sum((int)s.blocks, p.d, p.partial, dweight, stream);
 }
 
 }  // namespace
@@ -345,7 +415,7 @@ cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t stream) {
 size_t rmsnorm_backward_workspace_bytes(int B, int T, int d, ttt_dtype dtype) {
     if (B < 1 || T < 1 || d < 1 || d > kNormMaxWidth) return 0;
     const Shape s = backward_shape((long long)B * T, d, dtype == TTT_BF16 ? 2 : 4);
-    return (size_t)s.blocks * s.threads_y * d * sizeof(float);
+    return (size_t)s.blocks * d * sizeof(float);
 }
 
 cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a, float* workspace, cudaStream_t stream) {

@@ -22,7 +22,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 template <int V>
 __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[V]) {
-    static_assert(V == 1 || V == 4 || V == 8, "widths in use");
+    static_assert(V == 1 || V == 2 || V == 4 || V == 8, "widths in use");
     if constexpr (V == 8) {
         const uint4 r = *reinterpret_cast<const uint4*>(p);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -37,6 +37,10 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[V]) 
         v[1] = __uint_as_float(r.x & 0xffff0000u);
         v[2] = __uint_as_float(r.y << 16);
         v[3] = __uint_as_float(r.y & 0xffff0000u);
+    } else if constexpr (V == 2) {
+        const uint32_t r = *reinterpret_cast<const uint32_t*>(p);
+        v[0] = __uint_as_float(r << 16);
+        v[1] = __uint_as_float(r & 0xffff0000u);
     } else {
         v[0] = __bfloat162float(*p);
     }
@@ -44,9 +48,13 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&v)[V]) 
 
 template <int V>
 __device__ __forceinline__ void load_vec(const float* p, float (&v)[V]) {
-    static_assert(V == 1 || V == 4 || V == 8, "widths in use");
+    static_assert(V == 1 || V == 2 || V == 4 || V == 8, "widths in use");
     if constexpr (V == 1) {
         v[0] = *p;
+    } else if constexpr (V == 2) {
+        const float2 r = *reinterpret_cast<const float2*>(p);
+        v[0] = r.x;
+        v[1] = r.y;
     } else {
 #pragma unroll
         for (int i = 0; i < V / 4; i++) {
@@ -66,6 +74,8 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&v)[V])
             make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     } else if constexpr (V == 4) {
         *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16(v[0], v[1]);
     } else {
         *p = __float2bfloat16_rn(v[0]);
     }
@@ -75,11 +85,39 @@ template <int V>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
     if constexpr (V == 1) {
         *p = v[0];
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < V / 4; i++)
             reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     }
+}
+
+// Two floats in one 64-bit register pair, for the packed fp32 instructions of sm_100.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // A row's V elements as they come from memory, to be unpacked when they are used
@@ -141,6 +179,15 @@ struct Raw {
     }
 };
 
+// The same values as pairs (an even V)
+template <typename T, int V>
+__device__ __forceinline__ void pairs_of(const Raw<T, V>& r, f2 (&o)[V / 2]) {
+    float v[V];
+    r.get(v);
+#pragma unroll
+    for (int i = 0; i < V / 2; i++) o[i] = pack2(v[2 * i], v[2 * i + 1]);
+}
+
 // Elements [at, at + V) of a row of `width` that lie in it
 template <int V, typename T>
 __device__ __forceinline__ void store_within(T* row, int at, int width, const float (&v)[V]) {
@@ -169,7 +216,31 @@ __device__ __forceinline__ float rcp(float x) {
     return r;
 }
 
+// V neighbouring values as pairs (V = 1: one pair with a zero)
+template <int V>
+__device__ __forceinline__ void to_pairs(const float (&v)[V], f2 (&o)[(V + 1) / 2]) {
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; i++) o[i] = pack2(v[2 * i], 2 * i + 1 < V ? v[(2 * i + 1) % V] : 0.f);
+}
+template <int V>
+__device__ __forceinline__ void from_pairs(const f2 (&o)[(V + 1) / 2], float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; i++) {
+        float lo, hi;
+        unpack2(o[i], lo, hi);
+        v[2 * i] = lo;
+        if (2 * i + 1 < V) v[(2 * i + 1) % V] = hi;
+    }
+}
+
 // logistic function 1 / (1 + e^-x); at the ends e^-x is 0 or infinity and the result 1 or 0
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-1.4426950408889634f * x)); }
+
+__device__ __forceinline__ f2 sigmoid2(f2 x) {
+    float lo, hi;
+    unpack2(mul2(x, pack2(-1.4426950408889634f, -1.4426950408889634f)), lo, hi);
+    unpack2(add2(pack2(ex2(lo), ex2(hi)), pack2(1.f, 1.f)), lo, hi);
+    return pack2(rcp(lo), rcp(hi));
+}
 
 }  // namespace ttt
