@@ -494,13 +494,14 @@ class _Launch:
     """Device and stream of one call: makes the tensors' device current and, where a stream is given, allocates
     on it, so that the caching allocator knows which stream the call's buffers are used on."""
 
-    __slots__ = ("dev", "entered", "stream")
+    __slots__ = ("dev", "stream", "entered")
 
     def __init__(self, dev: torch.device, stream):
-        self.dev, self.stream, self.entered = dev, stream, ()
+        self.dev, self.stream = dev, stream
 
     def __enter__(self):
         dev = self.dev
+        self.entered = ()
         if dev.index != torch.cuda.current_device():
             self.entered = (torch.cuda.device(dev),)
         if self.stream is not None:
@@ -522,16 +523,22 @@ def _token_dtype(t: torch.Tensor, name: str) -> int:
     raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
 
 
-def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> Optional[int]:
-    """Address of a contiguous CUDA tensor of this shape, type and device (None for None)."""
-    if t is None:
-        return None
-    if t.get_device() != dev.index or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+def _refuse(t: torch.Tensor, name: str, shape, dtype, dev, what: str):
+    if t.get_device() != dev.index:
+        raise ValueError(f"{name} must be {what} on {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be {what} on {dev}, got strides {t.stride()}")
+
+
+def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> Optional[int]:
+    """Address of a contiguous CUDA tensor of this shape, type and device (None for None)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev.index or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, dev, "a contiguous CUDA tensor")
     return t.data_ptr()
 
 
@@ -539,18 +546,16 @@ def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
     """(address, row stride) of token rows [B, T, width], which may be a slice of wider rows."""
     if t is None:
         return None, 0
-    if t.get_device() != dev.index:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    what = "a CUDA tensor with its elements side by side and its rows at one distance"
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev.index:
+        _refuse(t, name, shape, dtype, dev, what)
     B, T, width = shape
+    if t.is_contiguous():
+        return t.data_ptr(), width
     sb, st, sw = t.stride()
     ld = st if T > 1 else (sb if B > 1 else width)
     if (sw != 1 and width > 1) or (B > 1 and T > 1 and sb != T * st) or (t.numel() and ld < width):
-        raise ValueError(f"{name} must have its elements side by side and its rows at one distance, "
-                         f"got strides {t.stride()}")
+        _refuse(t, name, shape, dtype, dev, what)
     return t.data_ptr(), max(ld, width)
 
 

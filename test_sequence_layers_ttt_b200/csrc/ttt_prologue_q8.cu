@@ -32,7 +32,8 @@ constexpr int kD = 64;               // head dimension
 constexpr int kBM = 128, kBK = 128;  // tile rows (tokens), K step per stage (bytes = elements)
 constexpr int kBN = 256;             // four heads of 64
 constexpr int kStages = 4;
-constexpr int kThreads = 256;
+constexpr int kEpilogue = 8;  // warps
+constexpr int kThreads = 128 + 32 * kEpilogue;
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 256 columns
 constexpr long long kTimeoutCycles = 2000000000LL;
 
@@ -43,7 +44,7 @@ struct alignas(1024) PStage {
 
 struct ProSmem {
     PStage st[kStages];
-    double inv_freq[kD / 2];  // base^(-2i/d)
+    double inv_turns[kD / 2];  // base^(-2i/d) / (2 pi)
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -74,20 +75,6 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, vol
             return false;
         }
     }
-}
-
-__device__ __forceinline__ void ld_32x32b_x32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, float (&v)[16]) {
@@ -134,13 +121,13 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         }
         for (int i = 0; i < 2; i++) {
             ptx::mbar_init(&s.acc_full[i], 1);
-            ptx::mbar_init(&s.acc_empty[i], 4);
+            ptx::mbar_init(&s.acc_empty[i], kEpilogue);
         }
         ptx::mbar_init(&s.drain, 1);
         ptx::fence_mbar_init();
     }
     if (warp == 1) tc05::tmem_alloc(ptx::smem_addr(&s.tmem_base), kTmemCols);
-    if (tid < kD / 2) s.inv_freq[tid] = exp2(-(2.0 * tid / kD) * log2((double)p.rope_base));
+    if (tid < kD / 2) s.inv_turns[tid] = exp2(-(2.0 * tid / kD) * log2((double)p.rope_base)) * 0.15915494309189535;
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
@@ -226,7 +213,7 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- epilogue
-        const int q = warp - 4;
+        const int q = warp % 4, half = (warp - 4) / 4;  // TMEM lanes 32 q ..; heads 2 half and 2 half + 1
         const uint32_t tq = tmem + tc05::taddr_lane(32 * q);
         const float inv_d = 1.f / kD;
         int local = 0;
@@ -243,7 +230,7 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             const float sx = valid ? p.scale_x[m] : 0.f;
             if (proj == 3) {
                 // learning-rate logits: columns 0..H-1
-                for (int c0 = 0; c0 < p.hp; c0 += 16) {  // hp is a multiple of 16, at most 256
+                for (int c0 = 16 * half; c0 < p.hp; c0 += 32) {  // hp is a multiple of 16, at most 256
                     float v[16];
                     ld_32x32b_x16(tacc + (uint32_t)c0, v);
                     tc05::wait_ld();
@@ -258,45 +245,52 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                 __nv_bfloat16* out = proj == 0 ? p.Q : proj == 1 ? p.K : p.V;
                 const float* sw = (proj == 0 ? p.scale_q : proj == 1 ? p.scale_k : p.scale_v) + grp * kBN;
                 const bool rope = p.rotary && proj < 2;
-                // the rotation of this token row, shared by the tile's four heads: angle
-                // pos * base^(-2i/d), reduced modulo 2 pi in double, then sin / cos in fp32
+                // the rotation of this token row, shared by the tile's four heads, times the token's scale: angle
+                // pos * base^(-2i/d), reduced to within pi in double, then sin and cos by the special-function
+                // unit (off by 5e-7 at most there, against the outputs' half step of 2^-8)
                 float cs[32], sn[32];
                 if (rope) {
                     const double pos = (double)(p.pos0 + t);
 #pragma unroll
                     for (int i = 0; i < 32; i++) {
-                        const double turns = pos * s.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
-                        const float r = (float)((turns - rint(turns)) * 6.283185307179586);
-                        sincosf(r, &sn[i], &cs[i]);
+                        const double turns = pos * s.inv_turns[i];
+                        const float r = (float)(turns - rint(turns)) * 6.283185307179586f;
+                        cs[i] = sx * __cosf(r);
+                        sn[i] = sx * __sinf(r);
                     }
                 }
-                for (int hh4 = 0; hh4 < 4; hh4++) {
-                    float x1[32], x2[32];  // features 0..31 and 32..63 of the head
-                    ld_32x32b_x32(tacc + (uint32_t)(64 * hh4), x1);
-                    ld_32x32b_x32(tacc + (uint32_t)(64 * hh4 + 32), x2);
-                    tc05::wait_ld();
+                for (int hh4 = 2 * half; hh4 < 2 * half + 2; hh4++) {
+                    uint4* dst = reinterpret_cast<uint4*>(out + (((size_t)bb * p.H + (4 * grp + hh4)) * p.T + t) * kD);
 #pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        x1[i] *= sx * sw[64 * hh4 + i];
-                        x2[i] *= sx * sw[64 * hh4 + 32 + i];
-                    }
-                    if (rope) {
+                    for (int f = 0; f < 32; f += 16) {  // features f .. f + 15 and their partners 32 further
+                        float x1[16], x2[16];
+                        ld_32x32b_x16(tacc + (uint32_t)(64 * hh4 + f), x1);
+                        ld_32x32b_x16(tacc + (uint32_t)(64 * hh4 + 32 + f), x2);
+                        const float4* w4 = reinterpret_cast<const float4*>(sw + 64 * hh4 + f);
+                        float wa[16], wb[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i++) {
-                            const float a = x1[i], b2 = x2[i];
-                            x1[i] = a * cs[i] - b2 * sn[i];
-                            x2[i] = b2 * cs[i] + a * sn[i];
+                        for (int i = 0; i < 4; i++) {
+                            const float4 a = w4[i], b = w4[8 + i];
+                            wa[4 * i] = a.x, wa[4 * i + 1] = a.y, wa[4 * i + 2] = a.z, wa[4 * i + 3] = a.w;
+                            wb[4 * i] = b.x, wb[4 * i + 1] = b.y, wb[4 * i + 2] = b.z, wb[4 * i + 3] = b.w;
                         }
-                    }
-                    if (valid) {
-                        uint4* dst = reinterpret_cast<uint4*>(
-                            out + (((size_t)bb * p.H + (4 * grp + hh4)) * p.T + t) * kD);
+                        tc05::wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 4; c++) {
-                            dst[c] = make_uint4(pack_rn(x1[8 * c + 0], x1[8 * c + 1]), pack_rn(x1[8 * c + 2], x1[8 * c + 3]),
-                                                pack_rn(x1[8 * c + 4], x1[8 * c + 5]), pack_rn(x1[8 * c + 6], x1[8 * c + 7]));
-                            dst[4 + c] = make_uint4(pack_rn(x2[8 * c + 0], x2[8 * c + 1]), pack_rn(x2[8 * c + 2], x2[8 * c + 3]),
-                                                    pack_rn(x2[8 * c + 4], x2[8 * c + 5]), pack_rn(x2[8 * c + 6], x2[8 * c + 7]));
+                        for (int k = 0; k < 16; k++) {
+                            const float u = x1[k] * wa[k], v = x2[k] * wb[k];
+                            x1[k] = rope ? u * cs[f + k] - v * sn[f + k] : u * sx;
+                            x2[k] = rope ? v * cs[f + k] + u * sn[f + k] : v * sx;
+                        }
+                        if (valid) {
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                dst[f / 8 + c] =
+                                    make_uint4(pack_rn(x1[8 * c + 0], x1[8 * c + 1]), pack_rn(x1[8 * c + 2], x1[8 * c + 3]),
+                                               pack_rn(x1[8 * c + 4], x1[8 * c + 5]), pack_rn(x1[8 * c + 6], x1[8 * c + 7]));
+                                dst[4 + f / 8 + c] =
+                                    make_uint4(pack_rn(x2[8 * c + 0], x2[8 * c + 1]), pack_rn(x2[8 * c + 2], x2[8 * c + 3]),
+                                               pack_rn(x2[8 * c + 4], x2[8 * c + 5]), pack_rn(x2[8 * c + 6], x2[8 * c + 7]));
+                            }
                         }
                     }
                 }

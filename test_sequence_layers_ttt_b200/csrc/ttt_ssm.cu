@@ -13,60 +13,70 @@ namespace {
 
 using namespace ssm;
 
+// Four neighbouring values of which the first `n` exist; kVec: all four, on a boundary of four
+template <bool kVec, typename T>
+__device__ __forceinline__ void load_four(const T* p, int n, float (&v)[kStates]) {
+    if constexpr (kVec) {
+        if (n > 0)
+            load_vec<kStates>(p, v);
+        else
+            v[0] = v[1] = v[2] = v[3] = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kStates; i++) v[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+}
+
 // A thread holds four states of one channel for the whole call; kLanes neighbouring lanes hold a
-// channel, and y is their sum.
-template <typename T, int kLanes>
+// channel, and y is their sum.  kVec: N is a multiple of four, and rows of B and C start on one.
+template <typename T, int kLanes, bool kVec>
 __global__ void __launch_bounds__(128) ttt_ssm_token_kernel(const Params p) {
     const long long id = (long long)blockIdx.x * 128 + threadIdx.x;
     const int part = threadIdx.x % kLanes;
     const long long bc = id / kLanes;
     const bool on = bc < (long long)p.B * p.C;
     const int b = on ? (int)(bc / p.C) : 0, c = on ? (int)(bc % p.C) : 0;
-    const int n0 = part * kStates;
-    const int len = on ? length_of(p.lengths, b, p.T) : 0;
+    const int n0 = part * kStates, live = on ? max(0, min(kStates, p.N - n0)) : 0;  // states that exist
     float h[kStates], a2[kStates];
-#pragma unroll
-    for (int i = 0; i < kStates; i++) {
-        const bool live = on && n0 + i < p.N;
-        a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
-        h[i] = live && p.h0 ? p.h0[(size_t)bc * p.N + n0 + i] : 0.f;
-    }
+    const size_t at = (size_t)bc * p.N + n0;
+    load_four<kVec>(p.h0 + at, live, h);
+    load_four<kVec>(p.A + (size_t)c * p.N + n0, live, a2);
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f, skip = on && p.D ? p.D[c] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kStates; i++) a2[i] *= kLog2e;
     for (int t = 0; t < p.T; t++) {
         const long long row = (long long)b * p.T + t;
-        float y = 0.f, u = 0.f;
-        if (t < len) {
-            float dt = to_f32(static_cast<const T*>(p.dt)[row * p.ld_dt + c]) + bias;
-            if (p.softplus) dt = ssm::softplus(dt);
+        float Bt[kStates], Ct[kStates], dt = 0.f, u = 0.f, z = 0.f;
+        load_four<kVec>(static_cast<const T*>(p.Bm) + row * p.ld_b + n0, live, Bt);
+        load_four<kVec>(static_cast<const T*>(p.Cm) + row * p.ld_c + n0, live, Ct);
+        if (on) {
+            dt = to_f32(static_cast<const T*>(p.dt)[row * p.ld_dt + c]) + bias;
             u = to_f32(static_cast<const T*>(p.u)[row * p.ld_u + c]);
-            const float du = dt * u;
-            const T* Bt = static_cast<const T*>(p.Bm) + row * p.ld_b;
-            const T* Ct = static_cast<const T*>(p.Cm) + row * p.ld_c;
+            if (p.z) z = to_f32(static_cast<const T*>(p.z)[row * p.ld_z + c]);
+        }
+        if (p.softplus) dt = ssm::softplus(dt);
+        const float du = dt * u;
+        float y = 0.f;
 #pragma unroll
-            for (int i = 0; i < kStates; i++) {
-                if (n0 + i < p.N) {
-                    h[i] = fmaf(decay(dt * a2[i]), h[i], du * to_f32(Bt[n0 + i]));
-                    y = fmaf(to_f32(Ct[n0 + i]), h[i], y);
-                }
-            }
+        for (int i = 0; i < kStates; i++) {
+            h[i] = fmaf(decay(dt * a2[i]), h[i], du * Bt[i]);
+            y = fmaf(Ct[i], h[i], y);
         }
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
         if (on && part == 0) {
-            if (t < len) {
-                y = fmaf(skip, u, y);
-                if (p.z) {
-                    const float z = to_f32(static_cast<const T*>(p.z)[row * p.ld_z + c]);
-                    y *= z * sigmoid(z);
-                }
-            }
-            const float out[1] = {y};
+            y = fmaf(skip, u, y);
+            const float out[1] = {p.z ? y * (z * sigmoid(z)) : y};
             store_vec<1>(static_cast<T*>(p.y) + row * p.C + c, out);
         }
     }
+    if constexpr (kVec) {
+        if (live > 0) store_vec<kStates>(p.h_T + at, h);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kStates; i++)
-        if (on && n0 + i < p.N) p.h_T[(size_t)bc * p.N + n0 + i] = h[i];
+        for (int i = 0; i < kStates; i++)
+            if (i < live) p.h_T[at + i] = h[i];
+    }
 }
 
 template <typename T>
@@ -77,12 +87,25 @@ cudaError_t launch_token(const SsmArgs& a, cudaStream_t stream) {
     const long long blocks = ((long long)a.B * a.C * lanes + 127) / 128;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
     const unsigned g = (unsigned)blocks;
+    const auto four = [](const void* q, long long ld) {
+        return reinterpret_cast<uintptr_t>(q) % (4 * sizeof(T)) == 0 && ld % 4 == 0;
+    };
+    if (a.N % 4 == 0 && four(a.Bm, a.ld_b) && four(a.Cm, a.ld_c)) {
+        switch (lanes) {
+            case 1: ttt_ssm_token_kernel<T, 1, true><<<g, 128, 0, stream>>>(p); break;
+            case 2: ttt_ssm_token_kernel<T, 2, true><<<g, 128, 0, stream>>>(p); break;
+            case 4: ttt_ssm_token_kernel<T, 4, true><<<g, 128, 0, stream>>>(p); break;
+            case 8: ttt_ssm_token_kernel<T, 8, true><<<g, 128, 0, stream>>>(p); break;
+            default: ttt_ssm_token_kernel<T, 16, true><<<g, 128, 0, stream>>>(p); break;
+        }
+        return cudaPeekAtLastError();
+    }
     switch (lanes) {
-        case 1: ttt_ssm_token_kernel<T, 1><<<g, 128, 0, stream>>>(p); break;
-        case 2: ttt_ssm_token_kernel<T, 2><<<g, 128, 0, stream>>>(p); break;
-        case 4: ttt_ssm_token_kernel<T, 4><<<g, 128, 0, stream>>>(p); break;
-        case 8: ttt_ssm_token_kernel<T, 8><<<g, 128, 0, stream>>>(p); break;
-        default: ttt_ssm_token_kernel<T, 16><<<g, 128, 0, stream>>>(p); break;
+        case 1: ttt_ssm_token_kernel<T, 1, false><<<g, 128, 0, stream>>>(p); break;
+        case 2: ttt_ssm_token_kernel<T, 2, false><<<g, 128, 0, stream>>>(p); break;
+        case 4: ttt_ssm_token_kernel<T, 4, false><<<g, 128, 0, stream>>>(p); break;
+        case 8: ttt_ssm_token_kernel<T, 8, false><<<g, 128, 0, stream>>>(p); break;
+        default: ttt_ssm_token_kernel<T, 16, false><<<g, 128, 0, stream>>>(p); break;
     }
     return cudaPeekAtLastError();
 }
