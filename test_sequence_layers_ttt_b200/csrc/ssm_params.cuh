@@ -66,15 +66,27 @@ template <typename T, bool kVec>
 __device__ __forceinline__ void stage_rows(T* dst, const T* src, long long ld, int t0, int rows, int len, int cols, int width,
                                            int tid, int threads) {
     constexpr int kV = kVec ? 16 / (int)sizeof(T) : 1;
-    const int per = cols / kV, shift = 31 - __clz(per);
-    for (int i = tid; i < rows * per; i += threads) {
-        const int r = i >> shift, c = (i & (per - 1)) * kV;
-        const bool live = t0 + r < len && c < width;
-        const T* from = live ? src + (long long)(t0 + r) * ld + c : src;
+    const int per = cols / kV, shift = 31 - __clz(per);  // pieces a row
+    const auto put = [](T* to, const T* from, bool live) {
         if constexpr (kVec || sizeof(T) == 4)
-            copy_async<kVec ? 16 : 4>(dst + r * cols + c, from, live);
+            copy_async<kVec ? 16 : 4>(to, from, live);
         else
-            dst[r * cols + c] = live ? *from : T(0.f);
+            *to = live ? *from : T(0.f);
+    };
+    if (per <= 32) {  // a thread keeps its column: `threads` is a multiple of 32
+        const int c = (tid & (per - 1)) * kV, step = threads >> shift;
+        int r = tid >> shift;
+        const T* from = src + (long long)(t0 + r) * ld + c;
+        T* to = dst + r * cols + c;
+        const long long advance = step * ld;
+        const int last = c < width ? len - t0 : 0;
+        for (; r < rows; r += step, from += advance, to += step * cols) put(to, r < last ? from : src, r < last);
+    } else {
+        for (int i = tid; i < rows * per; i += threads) {
+            const int r = i >> shift, c = (i & (per - 1)) * kV;
+            const bool live = t0 + r < len && c < width;
+            put(dst + r * cols + c, live ? src + (long long)(t0 + r) * ld + c : src, live);
+        }
     }
 }
 

@@ -7,8 +7,8 @@
 //   dA = sum_t g_t a_t h_{t-1} dt_t,  dD = sum_t dy'_t u_t,  dz_t = dy_t silu'(z_t) (C_t . h_t + D u_t)
 //
 // Two passes.  The first runs the scan and writes the state at the start of every chunk of kK tokens;
-// the second takes the chunks from the last to the first: it recomputes a chunk's decays and states into
-// registers and then walks it backwards.  A warp's lanes are 32 channels and a thread holds four states
+// the second takes the chunks from the last to the first: it recomputes a chunk's decays into registers and its
+// states into shared memory and then walks it backwards.  A warp's lanes are 32 channels and a thread holds four states
 // of one, so that B and C are one broadcast read each; the warps of a block share out the states.  Sums
 // over states meet in shared memory, sums over the block's channels in shuffles; what is summed over
 // blocks or sequences goes through the workspace and is added up in an order that the shape fixes.
@@ -171,12 +171,17 @@ struct BwdSmem {
     float b[kStates * kNW][kK + 4], c[kStates * kNW][kK + 4];
     float4 dt[kK / 4][32], du[kK / 4][32], dy[kK / 4][32];  // dt, dt u, dy'
     float4 slope[kK / 4][32], dyz[kK / 4][32];              // d dt / d raw, dy silu'(z)
-    float4 gb[kNW][kK / 4][32], ga[kNW][kK / 4][32], y[kNW][kK / 4][32];
+    // a thread's states after each token, four tokens of a state together; once a quad has been walked back, its
+    // first three places hold the thread's parts of g . B, of the sum with A, and of C . h
+    float4 h[kK / 4][kStates][32 * kNW];
     float sum[kNW][2][32];
 };
+// Blocks an SM of the second pass: 384 threads with 168 registers each (the decays of a chunk are 64 of them),
+// where keeping the states there too left room for 256.
+constexpr int blocks_for(int kNW) { return kNW >= 8 ? 1 : 12 / kNW; }
 
 template <typename T, int kNW, int kK, bool kVecRows, bool kVecBC>
-__global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwdParams p) {
+__global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_kernel(const SsmBwdParams p) {
     constexpr int kNp = kStates * kNW, kQ = kK / 4, kThreads = 32 * kNW;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     BwdSmem<T, kNW, kK>& s = *reinterpret_cast<BwdSmem<T, kNW, kK>*>(smem_raw);
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
             s.c[i % kNp][i / kNp] = to_f32(r.c[i / kNp][i % kNp]);
         }
         __syncthreads();
-        float a[kStates][kK], h[kStates][kK + 1];
+        float a[kStates][kK], start[kStates];
         {
             f2 dt[2 * kQ], du[2 * kQ];
 #pragma unroll
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
                 for (int k = 0; k < 2 * kQ; k++) x[k] = mul2(dt[k], A2);
                 decays<2 * kQ>(a[i], x);
                 const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][0]);
-                h[i][0] = first[i];
+                float h = start[i] = first[i];
 #pragma unroll
                 for (int q = 0; q < kQ; q++) {
                     const ulonglong2 Bq = Bi[q];
@@ -294,13 +299,15 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
                     unpack2(mul2(du[2 * q], Bq.x), v[0], v[1]);
                     unpack2(mul2(du[2 * q + 1], Bq.y), v[2], v[3]);
 #pragma unroll
-                    for (int k = 0; k < 4; k++) h[i][4 * q + k + 1] = fmaf(a[i][4 * q + k], h[i][4 * q + k], v[k]);
+                    for (int k = 0; k < 4; k++) v[k] = h = fmaf(a[i][4 * q + k], h, v[k]);
+                    s.h[q][i][tid] = make_float4(v[0], v[1], v[2], v[3]);
                 }
             }
         }
         if (chunk > 0) load_first(chunk - 1);
 #pragma unroll
         for (int q = kQ - 1; q >= 0; q--) {
+            asm volatile("" ::: "memory");  // the loads of one quad at a time: hoisted together they spill
             float v[32];  // of four tokens: dB and dC of the thread's four states
             const ulonglong2 dt = *reinterpret_cast<const ulonglong2*>(&s.dt[q][lane]);
             const ulonglong2 du = *reinterpret_cast<const ulonglong2*>(&s.du[q][lane]);
@@ -313,6 +320,8 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
             for (int i = 0; i < kStates; i++) {
                 const ulonglong2 Bq = *reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][4 * q]);
                 const ulonglong2 Cq = *reinterpret_cast<const ulonglong2*>(&s.c[n0 + i][4 * q]);
+                const float4 after = s.h[q][i][tid];
+                const float before[4] = {q > 0 ? s.h[(q + kQ - 1) % kQ][i][tid].w : start[i], after.x, after.y, after.z};
                 float ct[4], gk[4], x[4];
                 unpack2(Cq.x, ct[0], ct[1]);
                 unpack2(Cq.y, ct[2], ct[3]);
@@ -320,10 +329,10 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
                 for (int k = 3; k >= 0; k--) {
                     gk[k] = fmaf(ct[k], d[k], g[i]);
                     g[i] = gk[k] * a[i][4 * q + k];
-                    x[k] = g[i] * h[i][4 * q + k];
+                    x[k] = g[i] * before[k];
                 }
                 const f2 g0 = pack2(gk[0], gk[1]), g1 = pack2(gk[2], gk[3]);
-                const f2 h0 = pack2(h[i][4 * q + 1], h[i][4 * q + 2]), h1 = pack2(h[i][4 * q + 3], h[i][4 * q + 4]);
+                const f2 h0 = pack2(after.x, after.y), h1 = pack2(after.z, after.w);
                 const f2 x0 = pack2(x[0], x[1]), x1 = pack2(x[2], x[3]), A2 = pack2(a2[i], a2[i]);
                 unpack2(mul2(g0, du.x), v[i], v[8 + i]);
                 unpack2(mul2(g1, du.y), v[16 + i], v[24 + i]);
@@ -339,9 +348,9 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
                 unpack2(fma2(x1, dt.y, mul2(x0, dt.x)), lo, hi);
                 dA[i] += lo + hi;
             }
-            *reinterpret_cast<ulonglong2*>(&s.gb[warp][q][lane]) = make_ulonglong2(gb[0], gb[1]);
-            *reinterpret_cast<ulonglong2*>(&s.ga[warp][q][lane]) = make_ulonglong2(ga[0], ga[1]);
-            *reinterpret_cast<ulonglong2*>(&s.y[warp][q][lane]) = make_ulonglong2(y[0], y[1]);
+            *reinterpret_cast<ulonglong2*>(&s.h[q][0][tid]) = make_ulonglong2(gb[0], gb[1]);
+            *reinterpret_cast<ulonglong2*>(&s.h[q][1][tid]) = make_ulonglong2(ga[0], ga[1]);
+            *reinterpret_cast<ulonglong2*>(&s.h[q][2][tid]) = make_ulonglong2(y[0], y[1]);
             const float sum = sum_scatter(v, lane);
             const int t = chunk * kK + 4 * q + (lane >> 3), n = n0 + (lane & 3);
             if (t < len && n < p.N)
@@ -349,10 +358,11 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_backward_kernel(const SsmBwd
         }
         __syncthreads();
         for (int q = warp; q < kQ; q += kNW) {
-            float4 gb = s.gb[0][q][lane], ga = s.ga[0][q][lane], y = s.y[0][q][lane];
+            float4 gb = s.h[q][0][lane], ga = s.h[q][1][lane], y = s.h[q][2][lane];
 #pragma unroll
             for (int k = 1; k < kNW; k++) {
-                const float4 b4 = s.gb[k][q][lane], a4 = s.ga[k][q][lane], y4 = s.y[k][q][lane];
+                const int from = 32 * k + lane;
+                const float4 b4 = s.h[q][0][from], a4 = s.h[q][1][from], y4 = s.h[q][2][from];
                 gb = make_float4(gb.x + b4.x, gb.y + b4.y, gb.z + b4.z, gb.w + b4.w);
                 ga = make_float4(ga.x + a4.x, ga.y + a4.y, ga.z + a4.z, ga.w + a4.w);
                 y = make_float4(y.x + y4.x, y.y + y4.y, y.z + y4.z, y.w + y4.w);
@@ -438,7 +448,7 @@ __global__ void __launch_bounds__(256) ttt_ssm_channel_sum_kernel(int B, int C, 
 }
 
 constexpr int warps_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-// 16 tokens a chunk keep 128 values in registers; with 16 warps a thread has 128 registers, so 8 there
+// 16 tokens a chunk keep 64 decays in registers; with 16 warps a thread has 128 registers in all, so 8 there
 constexpr int chunk_for(int kNW) { return kNW <= 8 ? 16 : 8; }
 
 struct Layout {
@@ -480,7 +490,8 @@ cudaError_t by_alignment(const SsmBwdParams& p, cudaStream_t stream) {
     const bool rows = rows16(p.u, p.ld_u, p.C, es) && rows16(p.dt, p.ld_dt, p.C, es) && rows16(p.z, p.ld_z, p.C, es) &&
                       rows16(p.dy, p.C, p.C, es);
     const bool bc = rows16(p.Bm, p.ld_b, p.N, es) && rows16(p.Cm, p.ld_c, p.N, es);
-    if (rows && bc) return launch<T, kNW, true, true>(p, stream);
+    if constexpr (kNW * kStates * es >= 16)  // else a row of B is no whole unit at any N
+        if (rows && bc) return launch<T, kNW, true, true>(p, stream);
     if (rows) return launch<T, kNW, true, false>(p, stream);
     return launch<T, kNW, false, false>(p, stream);
 }

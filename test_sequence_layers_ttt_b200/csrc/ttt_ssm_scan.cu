@@ -229,7 +229,8 @@ cudaError_t launch(const SsmArgs& a, cudaStream_t stream) {
         kernel<<<(unsigned)grid, 32 * (kWarps + kHelpers), smem, stream>>>(p, (int)cblocks);
         return cudaPeekAtLastError();
     };
-    if (rows && bc) return run(ttt_ssm_scan_kernel<T, kWarps, true, true>);
+    if constexpr (kWarps * kStates * es >= 16)  // else a row of B is no whole unit at any N
+        if (rows && bc) return run(ttt_ssm_scan_kernel<T, kWarps, true, true>);
     if (rows) return run(ttt_ssm_scan_kernel<T, kWarps, true, false>);
     return run(ttt_ssm_scan_kernel<T, kWarps, false, false>);
 }
