@@ -5,7 +5,7 @@
 // over d_model is of exact products in fp32, and the scales, constant along it, multiply the accumulator in
 // the epilogue, before the rotary embedding (of Q and K) or the sigmoid gate.  Column tiles of 256 hold four
 // heads of one of Q, K, V; one more tile of round16(H) columns holds the H learning-rate logits.  Persistent
-// CTAs of 8 warps walk the tiles (column tiles fastest, so the CTAs in flight share each row tile in L2):
+// CTAs of 12 warps walk the tiles (column tiles fastest, so the CTAs in flight share each row tile in L2):
 //   warp 0     TMA loads of x (128 x 128) and weight (256 x 128) tiles, 4-stage ring; past d_model a box
 //              reads zeros
 //   warp 1     TMEM allocation and the tcgen05 MMAs (kind f8f6f4, M = 128, N = 256, K = 32), fp32
@@ -21,6 +21,7 @@
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 #include "tma_host.h"
+#include "vec_io.cuh"
 
 namespace ttt {
 
@@ -44,7 +45,8 @@ struct alignas(1024) PStage {
 
 struct ProSmem {
     PStage st[kStages];
-    double inv_turns[kD / 2];  // base^(-2i/d) / (2 pi)
+    unsigned char out[kEpilogue][32 * kD * 2];  // a warp's rows of one head on their way out, 128-byte swizzle
+    unsigned long long turn[kD / 2];  // base^(-2i/d) / (2 pi), in turns of 2^64
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -89,10 +91,17 @@ __device__ __forceinline__ void ld_32x32b_x16(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+// A box of shared memory (the generic proxy's writes of it fenced) to global memory; rows past the tensor's end
+// are left out.  One thread; `read_out` waits until the shared memory may be written again, `all_out` for the
+// stores themselves.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
+                 "r"(ptx::smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void read_out() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void all_out() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 struct PrologueQ8Params {
     int B, T, H, d_model, pos0, rotary, n_col_tiles, n_tiles, hp;  // hp: H rounded up to 16
@@ -105,7 +114,9 @@ struct PrologueQ8Params {
 __global__ void __launch_bounds__(kThreads, 1)
 ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmWq,
                        const __grid_constant__ CUtensorMap tmWk, const __grid_constant__ CUtensorMap tmWv,
-                       const __grid_constant__ CUtensorMap tmWl, const PrologueQ8Params p) {
+                       const __grid_constant__ CUtensorMap tmWl, const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const PrologueQ8Params p) {
     extern __shared__ unsigned char smem_raw[];
     ProSmem& s = *reinterpret_cast<ProSmem*>(smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -127,7 +138,7 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         ptx::fence_mbar_init();
     }
     if (warp == 1) tc05::tmem_alloc(ptx::smem_addr(&s.tmem_base), kTmemCols);
-    if (tid < kD / 2) s.inv_turns[tid] = exp2(-(2.0 * tid / kD) * log2((double)p.rope_base)) * 0.15915494309189535;
+    if (tid < kD / 2) s.turn[tid] = (unsigned long long)(exp2(64.0 - (2.0 * tid / kD) * log2((double)p.rope_base)) * 0.15915494309189535);
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
@@ -246,52 +257,92 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                 const float* sw = (proj == 0 ? p.scale_q : proj == 1 ? p.scale_k : p.scale_v) + grp * kBN;
                 const bool rope = p.rotary && proj < 2;
                 // the rotation of this token row, shared by the tile's four heads, times the token's scale: angle
-                // pos * base^(-2i/d), reduced to within pi in double, then sin and cos by the special-function
-                // unit (off by 5e-7 at most there, against the outputs' half step of 2^-8)
-                float cs[32], sn[32];
+                // pos * base^(-2i/d) in fixed point, whose overflow leaves whole turns out, then sin and cos by the
+                // special-function unit: the angle is off by 4e-7 and they by 5e-7 at most, against the outputs'
+                // half step of 2^-8.  (In double the reduction took as long as both functions.)
+                f2 cs[16], sn[16];  // of two neighbouring features each
                 if (rope) {
-                    const double pos = (double)(p.pos0 + t);
+                    const unsigned long long pos = (unsigned long long)(long long)(p.pos0 + t);
 #pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const double turns = pos * s.inv_turns[i];
-                        const float r = (float)(turns - rint(turns)) * 6.283185307179586f;
-                        cs[i] = sx * __cosf(r);
-                        sn[i] = sx * __sinf(r);
+                    for (int i = 0; i < 16; i++) {
+                        float c[2], n[2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            // the fraction of a turn, exact to 2^-46; its top 23 bits become a float in [-1/2, 1/2)
+                            const uint32_t phase = (uint32_t)((pos * s.turn[2 * i + k]) >> 32) + 0x80000000u;
+                            const float r = (__uint_as_float(0x3f800000u | (phase >> 9)) - 1.5f) * 6.283185307179586f;
+                            c[k] = sx * __cosf(r);
+                            n[k] = sx * __sinf(r);
+                        }
+                        cs[i] = pack2(c[0], c[1]);
+                        sn[i] = pack2(n[0], n[1]);
                     }
                 }
+                // The warp's rows are neighbours in Q, K, V unless a sequence ends among them: then one box
+                // takes a head's rows out, and rows past the sequence's (and the batch's) end fall away.
+                const int bb0 = __shfl_sync(0xffffffffu, bb, 0), t0 = __shfl_sync(0xffffffffu, t, 0);
+                const bool one_box = __all_sync(0xffffffffu, !valid || bb == bb0) && mt * kBM + 32 * q < M;
+                const void* tmO = proj == 0 ? &tmQ : proj == 1 ? &tmK : &tmV;
+                unsigned char* stage = s.out[warp - 4];
+                const f2 sx2 = pack2(sx, sx), minus = pack2(-1.f, -1.f);
                 for (int hh4 = 2 * half; hh4 < 2 * half + 2; hh4++) {
-                    uint4* dst = reinterpret_cast<uint4*>(out + (((size_t)bb * p.H + (4 * grp + hh4)) * p.T + t) * kD);
+                    const int head = 4 * grp + hh4;
+                    uint4* dst = reinterpret_cast<uint4*>(out + (((size_t)bb * p.H + head) * p.T + t) * kD);
+                    if (lane == 0) read_out();
+                    __syncwarp();
 #pragma unroll
                     for (int f = 0; f < 32; f += 16) {  // features f .. f + 15 and their partners 32 further
                         float x1[16], x2[16];
                         ld_32x32b_x16(tacc + (uint32_t)(64 * hh4 + f), x1);
                         ld_32x32b_x16(tacc + (uint32_t)(64 * hh4 + 32 + f), x2);
-                        const float4* w4 = reinterpret_cast<const float4*>(sw + 64 * hh4 + f);
-                        float wa[16], wb[16];
+                        const ulonglong2* w4 = reinterpret_cast<const ulonglong2*>(sw + 64 * hh4 + f);
+                        f2 wa[8], wb[8];
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            const float4 a = w4[i], b = w4[8 + i];
-                            wa[4 * i] = a.x, wa[4 * i + 1] = a.y, wa[4 * i + 2] = a.z, wa[4 * i + 3] = a.w;
-                            wb[4 * i] = b.x, wb[4 * i + 1] = b.y, wb[4 * i + 2] = b.z, wb[4 * i + 3] = b.w;
+                            const ulonglong2 a = w4[i], b = w4[8 + i];
+                            wa[2 * i] = a.x;
+                            wa[2 * i + 1] = a.y;
+                            wb[2 * i] = b.x;
+                            wb[2 * i + 1] = b.y;
                         }
                         tc05::wait_ld();
+                        uint32_t o1[8], o2[8];
 #pragma unroll
-                        for (int k = 0; k < 16; k++) {
-                            const float u = x1[k] * wa[k], v = x2[k] * wb[k];
-                            x1[k] = rope ? u * cs[f + k] - v * sn[f + k] : u * sx;
-                            x2[k] = rope ? v * cs[f + k] + u * sn[f + k] : v * sx;
+                        for (int k = 0; k < 8; k++) {
+                            const f2 u = mul2(pack2(x1[2 * k], x1[2 * k + 1]), wa[k]);
+                            const f2 v = mul2(pack2(x2[2 * k], x2[2 * k + 1]), wb[k]);
+                            f2 y1, y2;
+                            if (rope) {
+                                const f2 c = cs[f / 2 + k], n = sn[f / 2 + k];
+                                y1 = fma2(mul2(v, minus), n, mul2(u, c));
+                                y2 = fma2(u, n, mul2(v, c));
+                            } else {
+                                y1 = mul2(u, sx2);
+                                y2 = mul2(v, sx2);
+                            }
+                            float lo, hi;
+                            unpack2(y1, lo, hi);
+                            o1[k] = pack_bf16(lo, hi);
+                            unpack2(y2, lo, hi);
+                            o2[k] = pack_bf16(lo, hi);
                         }
-                        if (valid) {
 #pragma unroll
-                            for (int c = 0; c < 2; c++) {
-                                dst[f / 8 + c] =
-                                    make_uint4(pack_rn(x1[8 * c + 0], x1[8 * c + 1]), pack_rn(x1[8 * c + 2], x1[8 * c + 3]),
-                                               pack_rn(x1[8 * c + 4], x1[8 * c + 5]), pack_rn(x1[8 * c + 6], x1[8 * c + 7]));
-                                dst[4 + f / 8 + c] =
-                                    make_uint4(pack_rn(x2[8 * c + 0], x2[8 * c + 1]), pack_rn(x2[8 * c + 2], x2[8 * c + 3]),
-                                               pack_rn(x2[8 * c + 4], x2[8 * c + 5]), pack_rn(x2[8 * c + 6], x2[8 * c + 7]));
+                        for (int c = 0; c < 2; c++) {  // 16-byte chunks f / 8 + c and 4 + f / 8 + c of the row
+                            const uint4 a = make_uint4(o1[4 * c], o1[4 * c + 1], o1[4 * c + 2], o1[4 * c + 3]);
+                            const uint4 b = make_uint4(o2[4 * c], o2[4 * c + 1], o2[4 * c + 2], o2[4 * c + 3]);
+                            if (one_box) {
+                                *reinterpret_cast<uint4*>(stage + lane * 128 + (((f / 8 + c) ^ (lane & 7)) * 16)) = a;
+                                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 + f / 8 + c) ^ (lane & 7)) * 16)) = b;
+                            } else if (valid) {
+                                dst[f / 8 + c] = a;
+                                dst[4 + f / 8 + c] = b;
                             }
                         }
+                    }
+                    if (one_box) {
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tma_store_3d(tmO, stage, 0, t0, bb0 * p.H + head);
                     }
                 }
             }
@@ -299,6 +350,7 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.acc_empty[buf]);
         }
+        if (lane == 0) all_out();
     }
     tc05::fence_before_sync();
     __syncthreads();
@@ -319,6 +371,18 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [BH][T][64] bf16 in boxes of [1][32][64] with the 128-byte swizzle
+bool make_out_map(CUtensorMap* m, void* base, int T, long long BH) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {kD, (cuuint64_t)T, (cuuint64_t)BH};
+    cuuint64_t strides[2] = {kD * 2, (cuuint64_t)T * kD * 2};
+    cuuint32_t box[3] = {kD, 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 bool prologue_q8_supports(int B, int T, int H, int d, int d_model) {
@@ -335,6 +399,10 @@ cudaError_t launch_prologue_q8(const PrologueArgs& a, const PrologueScales& s, c
     if (!make_map(&mx, a.x, dm, (uint64_t)M, kBM) || !make_map(&mq, a.theta_q, dm, features, kBN) ||
         !make_map(&mk, a.theta_k, dm, features, kBN) || !make_map(&mv, a.theta_v, dm, features, kBN) ||
         !make_map(&ml, a.theta_lr, dm, (uint64_t)a.H, (uint32_t)hp))
+        return cudaErrorInvalidValue;
+    CUtensorMap oq, ok, ov;
+    const long long BH = (long long)a.B * a.H;
+    if (!make_out_map(&oq, a.Q, a.T, BH) || !make_out_map(&ok, a.K, a.T, BH) || !make_out_map(&ov, a.V, a.T, BH))
         return cudaErrorInvalidValue;
     PrologueQ8Params p{};
     p.B = a.B;
@@ -364,7 +432,7 @@ cudaError_t launch_prologue_q8(const PrologueArgs& a, const PrologueScales& s, c
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int grid = p.n_tiles < sms ? p.n_tiles : sms;
-    ttt_prologue_q8_kernel<<<grid, kThreads, smem, stream>>>(mx, mq, mk, mv, ml, p);
+    ttt_prologue_q8_kernel<<<grid, kThreads, smem, stream>>>(mx, mq, mk, mv, ml, oq, ok, ov, p);
     return cudaPeekAtLastError();
 }
 
