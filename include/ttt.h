@@ -360,6 +360,7 @@ ttt_status ttt_linear_backward_static(int B, int H, int T, int d, int mini_batch
  * follows T * ld elements later), so a slice of a wider projection can be
  * passed as it is; they need the alignment of their element only, every other
  * pointer 16 bytes.  Rows on 16-byte boundaries are read 16 bytes at a time.
+ * B T stays below 2^31 - 2^16 (TTT_ERR_SHAPE).
  * lengths (or NULL) is a DEVICE array of B token counts for a padded batch:
  * tokens at or past lengths[b] (taken into 0..T) are not read, leave the state
  * as it is and have zeros as their outputs and gradients.
@@ -476,16 +477,14 @@ ttt_status ttt_conv_backward(int B, int T, int C, int width, ttt_dtype dtype, in
  *   h0       [B][C][N] fp32 or NULL (zero)
  *   y        [B][T][C];  h_T  [B][C][N] fp32: the state after each sequence's
  *            last token; may be the same pointer as h0
- * T >= 0.  workspace as in ttt_linear_backward; its size may be 0, and then
- * it may be NULL.
+ * T >= 0.
  */
-size_t ttt_ssm_forward_workspace_size(int B, int T, int C, int N);
 ttt_status ttt_ssm_forward(int B, int T, int C, int N, ttt_dtype dtype, int dt_softplus, long long ld_u,
                            long long ld_dt, long long ld_b, long long ld_c, long long ld_z,
                            const void* u, const void* dt, const float* dt_bias, const float* A,
                            const void* Bm, const void* Cm, const float* D, const void* z,
-                           const float* h0, const int* lengths, void* y, float* h_T, void* workspace,
-                           size_t workspace_bytes, ttt_stream_t stream);
+                           const float* h0, const int* lengths, void* y, float* h_T,
+                           ttt_stream_t stream);
 
 /* The scan continued by T >= 0 more tokens, one at a time in serving: h is
  * read, then overwritten with the state after the call's last token. */

@@ -478,10 +478,8 @@ lib.ttt_conv_backward_workspace_size.restype = _Z
 lib.ttt_conv_backward_workspace_size.argtypes = [_I] * 4
 lib.ttt_conv_backward.restype = _I
 lib.ttt_conv_backward.argtypes = [_I] * 6 + [_L] + [_P] * 12 + [_Z, _P]
-lib.ttt_ssm_forward_workspace_size.restype = _Z
-lib.ttt_ssm_forward_workspace_size.argtypes = [_I] * 4
 lib.ttt_ssm_forward.restype = _I
-lib.ttt_ssm_forward.argtypes = [_I] * 6 + [_L] * 5 + [_P] * 13 + [_Z, _P]
+lib.ttt_ssm_forward.argtypes = [_I] * 6 + [_L] * 5 + [_P] * 12 + [_P]
 lib.ttt_ssm_decode.restype = _I
 lib.ttt_ssm_decode.argtypes = [_I] * 6 + [_L] * 5 + [_P] * 10 + [_P]
 lib.ttt_ssm_backward_workspace_size.restype = _Z
@@ -691,7 +689,7 @@ def ttt_conv_forward(x, weight, bias=None, state0=None, *, lengths=None, activat
     B, T, C, W, _ = shape
     dev, dt = x.device, x.dtype
     with _Launch(dev, stream) as s:
-        y = torch.empty((B, T, C), dtype=dt, device=dev) if y is None else y
+        y = x.new_empty((B, T, C)) if y is None else y
         state_T = torch.empty((B, W - 1, C), dtype=dt, device=dev) if state_T is None else state_T
         _check(lib.ttt_conv_forward(*shape, _silu_code(activation), ld, px, pw, pb, ps, pl,
                                     _dense(y, "y", (B, T, C), dt, dev),
@@ -708,7 +706,7 @@ def ttt_conv_decode(x, weight, bias, state, *, activation="silu", y=None, stream
     B, T, C, W, _ = shape
     dev, dt = x.device, x.dtype
     with _Launch(dev, stream) as s:
-        y = torch.empty((B, T, C), dtype=dt, device=dev) if y is None else y
+        y = x.new_empty((B, T, C)) if y is None else y
         _check(lib.ttt_conv_decode(*shape, _silu_code(activation), ld, px, pw, pb, ps,
                                    _dense(y, "y", (B, T, C), dt, dev), s))
     return y
@@ -753,21 +751,17 @@ def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, h_name="h0"):
 
 
 def ttt_ssm_forward(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, lengths=None, dt_softplus: bool = True,
-                    y=None, h_T=None, workspace=None, stream=None):
+                    y=None, h_T=None, stream=None):
     """Selective state space scan (see include/ttt.h).  u, dt, z [B, T, C] and Bm, Cm [B, T, N], bf16 or fp32 (slices
     of wider rows will do); A [C, N], D, dt_bias [C], h0 [B, C, N] fp32.  Returns (y, h_T)."""
     shape, lds, ptrs = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths)
     B, T, C, N, _ = shape
     dev = u.device
     with _Launch(dev, stream) as s:
-        y = torch.empty((B, T, C), dtype=u.dtype, device=dev) if y is None else y
+        y = u.new_empty((B, T, C)) if y is None else y
         h_T = torch.empty((B, C, N), dtype=torch.float32, device=dev) if h_T is None else h_T
-        need = lib.ttt_ssm_forward_workspace_size(B, T, C, N)
-        pws, n = None, 0
-        if need or workspace is not None:
-            workspace, pws, n = _workspace(workspace, need, dev)
         _check(lib.ttt_ssm_forward(*shape, int(bool(dt_softplus)), *lds, *ptrs, _dense(y, "y", (B, T, C), u.dtype, dev),
-                                   _dense(h_T, "h_T", (B, C, N), torch.float32, dev), pws, n, s))
+                                   _dense(h_T, "h_T", (B, C, N), torch.float32, dev), s))
     return y, h_T
 
 
@@ -779,7 +773,7 @@ def ttt_ssm_decode(u, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, *, dt_soft
     B, T, C, N, _ = shape
     dev = u.device
     with _Launch(dev, stream) as s:
-        y = torch.empty((B, T, C), dtype=u.dtype, device=dev) if y is None else y
+        y = u.new_empty((B, T, C)) if y is None else y
         _check(lib.ttt_ssm_decode(*shape, int(bool(dt_softplus)), *lds, *ptrs[:-1],
                                   _dense(y, "y", (B, T, C), u.dtype, dev), s))
     return y

@@ -5,6 +5,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,7 +18,7 @@ TIMELINE_LIB = os.path.join(PKG, "libttt_b200_timeline.so")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
 ]
 
@@ -38,13 +40,22 @@ def build(force: bool = False, verbose: bool = False, timeline: bool = False) ->
     nvcc = os.environ.get("NVCC", "nvcc")
     if not os.path.isabs(nvcc) and os.path.exists("/usr/local/cuda/bin/nvcc"):
         nvcc = "/usr/local/cuda/bin/nvcc"
-    tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, *(["-DTTT_TIMELINE"] if timeline else []), "-I", os.path.join(ROOT, "include"),
-           "-o", tmp, *sources()]
+    flags = [*NVCC_FLAGS, *(["-DTTT_TIMELINE"] if timeline else []), "-I", os.path.join(ROOT, "include")]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
+        flags.insert(0, "-Xptxas=-v")
+    tmp = out + f".tmp{os.getpid()}"
+    with tempfile.TemporaryDirectory() as work:  # one object a source, compiled side by side
+        def compile_one(src):
+            obj = os.path.join(work, os.path.basename(src) + ".o")
+            cmd = [nvcc, *flags, "-c", src, "-o", obj]
+            if verbose:
+                print(" ".join(cmd))
+            subprocess.run(cmd, check=True)
+            return obj
+
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            objects = list(pool.map(compile_one, sources()))
+        subprocess.run([nvcc, *NVCC_FLAGS[:2], "-shared", "-o", tmp, *objects], check=True)
     os.replace(tmp, out)
     return out
 

@@ -57,7 +57,7 @@ cudaError_t launch_conv(const ConvArgs& a, cudaStream_t stream);
 size_t conv_backward_workspace_bytes(int B, int T, int C, int W);
 cudaError_t launch_conv_backward(const ConvBwdArgs& a, float* workspace, cudaStream_t stream);
 
-// Selective state space scan (ttt_ssm.cu, ttt_ssm_backward.cu)
+// Selective state space scan (ttt_ssm.cu, ttt_ssm_scan.cu, ttt_ssm_segments.cu, ttt_ssm_backward.cu)
 constexpr int kSsmMaxStates = 64;
 struct SsmArgs {
     int B, T, C, N;
@@ -81,8 +81,7 @@ struct SsmBwdArgs {
     void *du, *ddt, *dz;
     float *dA, *dB, *dC, *dD, *ddt_bias, *dh0;
 };
-size_t ssm_forward_workspace_bytes(int B, int T, int C, int N);
-cudaError_t launch_ssm_forward(const SsmArgs& a, float* workspace, cudaStream_t stream);
+cudaError_t launch_ssm_forward(const SsmArgs& a, cudaStream_t stream);
 // in place on h_T (= h0), any number of tokens
 cudaError_t launch_ssm_token(const SsmArgs& a, cudaStream_t stream);
 size_t ssm_backward_workspace_bytes(int B, int T, int C, int N);

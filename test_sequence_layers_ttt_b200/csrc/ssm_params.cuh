@@ -21,7 +21,13 @@ struct Params {
     const int* lengths;
     void* y;
     float* h_T;
+    bool vec_rows, vec_bc;  // rows16 of u, dt and z, and of B and C
 };
+
+// Whether rows of `width` elements, `ld` apart, are whole 16-byte units on 16-byte boundaries
+inline bool rows16(const void* q, long long ld, int width, int es) {
+    return !q || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && (ld * es) % 16 == 0 && (width * es) % 16 == 0);
+}
 
 inline Params params_of(const SsmArgs& a) {
     Params p{};
@@ -47,6 +53,9 @@ inline Params params_of(const SsmArgs& a) {
     p.lengths = a.lengths;
     p.y = a.y;
     p.h_T = a.h_T;
+    const int es = a.dtype == TTT_BF16 ? 2 : 4;
+    p.vec_rows = rows16(a.u, a.ld_u, a.C, es) && rows16(a.dt, a.ld_dt, a.C, es) && rows16(a.z, a.ld_z, a.C, es);
+    p.vec_bc = rows16(a.Bm, a.ld_b, a.N, es) && rows16(a.Cm, a.ld_c, a.N, es);
     return p;
 }
 
@@ -59,14 +68,11 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool live
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
 
-// Rows [t0, t0 + rows) of `cols` (a power of two) columns into shared memory (row stride `cols`); rows at or
-// past `len` and columns at or past `width` become zeros and are not read.  kVec: 16 bytes a copy; else an
-// element, which for bf16 cp.async cannot copy.
 template <typename T, bool kVec>
-__device__ __forceinline__ void stage_rows(T* dst, const T* src, long long ld, int t0, int rows, int len, int cols, int width,
+__device__ __forceinline__ void stage_rows_by(T* dst, const T* src, long long ld, int t0, int rows, int len, int cols, int width,
                                            int tid, int threads) {
     constexpr int kV = kVec ? 16 / (int)sizeof(T) : 1;
-    const int per = cols / kV, shift = 31 - __clz(per);  // pieces a row
+    const int per = max(cols / kV, 1), shift = 31 - __clz(per);  // pieces a row
     const auto put = [](T* to, const T* from, bool live) {
         if constexpr (kVec || sizeof(T) == 4)
             copy_async<kVec ? 16 : 4>(to, from, live);
@@ -90,9 +96,16 @@ __device__ __forceinline__ void stage_rows(T* dst, const T* src, long long ld, i
     }
 }
 
-// Whether rows of `width` elements, `ld` apart, are whole 16-byte units on 16-byte boundaries
-inline bool rows16(const void* q, long long ld, int width, int es) {
-    return !q || (reinterpret_cast<uintptr_t>(q) % 16 == 0 && (ld * es) % 16 == 0 && (width * es) % 16 == 0);
+// Rows [t0, t0 + rows) of `cols` (a power of two) columns into shared memory (row stride `cols`); rows at or
+// past `len` and columns at or past `width` become zeros and are not read.  vec: 16 bytes a copy (rows16 of
+// the rows); else an element, which for bf16 cp.async cannot copy.
+template <typename T>
+__device__ __forceinline__ void stage_rows(bool vec, T* dst, const T* src, long long ld, int t0, int rows, int len, int cols,
+                                           int width, int tid, int threads) {
+    if (vec)
+        stage_rows_by<T, true>(dst, src, ld, t0, rows, len, cols, width, tid, threads);
+    else
+        stage_rows_by<T, false>(dst, src, ld, t0, rows, len, cols, width, tid, threads);
 }
 
 }  // namespace ssm

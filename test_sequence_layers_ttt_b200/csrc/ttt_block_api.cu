@@ -37,7 +37,8 @@ ttt_status no_overlap(const Span (&outs)[no], const int (&allowed)[no], const Sp
     return check_aliasing(outs, (int)no, ins, allowed, (int)ni);
 }
 
-bool tokens_fit(int B, int T) { return (long long)B * T < (1LL << 31); }
+// Token numbers, and those of the tile that one falls in, stay below 2^31
+bool tokens_fit(int B, int T) { return (long long)B * T < (1LL << 31) - (1LL << 16); }
 
 ttt_status launched(cudaError_t e, ttt_stream_t stream) { return finish(e, reinterpret_cast<cudaStream_t>(stream)); }
 
@@ -172,14 +173,12 @@ ttt_status check_ssm_inputs(const SsmArgs& a, Span (&ins)[10]) {
     return TTT_OK;
 }
 
-ttt_status check_ssm(const SsmArgs& a, const void* workspace, size_t workspace_bytes, size_t need) {
-    Span in[10];
-    ttt_status st = check_ssm_inputs(a, in);
+ttt_status check_ssm(const SsmArgs& a) {
+    Span ins[10];
+    ttt_status st = check_ssm_inputs(a, ins);
     if (st != TTT_OK) return st;
     if (!a.h_T || (a.T > 0 && !a.y)) return TTT_ERR_NULL;
-    if (any_unaligned({a.y, a.h_T, workspace})) return TTT_ERR_ALIGN;
-    if (need > 0 && (!workspace || workspace_bytes < need)) return TTT_ERR_WORKSPACE;
-    const Span ins[] = {in[0], in[1], in[2], in[3], in[4], in[5], in[6], in[7], in[8], in[9], {workspace, need}};
+    if (any_unaligned({a.y, a.h_T})) return TTT_ERR_ALIGN;
     const Span outs[] = {{a.y, (size_t)a.B * a.T * a.C * size_of(a.dtype)}, {a.h_T, (size_t)a.B * a.C * a.N * 4}};
     const int allowed[] = {-1, 0};
     return no_overlap(outs, allowed, ins);
@@ -293,19 +292,17 @@ ttt_status ttt_conv_backward(int B, int T, int C, int width, ttt_dtype dtype, in
                     stream);
 }
 
-size_t ttt_ssm_forward_workspace_size(int B, int T, int C, int N) { return ssm_forward_workspace_bytes(B, T, C, N); }
-
 ttt_status ttt_ssm_forward(int B, int T, int C, int N, ttt_dtype dtype, int dt_softplus, long long ld_u,
                            long long ld_dt, long long ld_b, long long ld_c, long long ld_z, const void* u,
                            const void* dt, const float* dt_bias, const float* A, const void* Bm, const void* Cm,
                            const float* D, const void* z, const float* h0, const int* lengths, void* y, float* h_T,
-                           void* workspace, size_t workspace_bytes, ttt_stream_t stream) {
+                           ttt_stream_t stream) {
     const SsmArgs a{B, T, C, N, dtype, dt_softplus, ld_u, ld_dt, ld_b, ld_c, ld_z, u, dt, dt_bias, A, Bm, Cm, D, z,
                     h0, lengths, y, h_T};
-    const ttt_status st = check_ssm(a, workspace, workspace_bytes, ssm_forward_workspace_bytes(B, T, C, N));
+    const ttt_status st = check_ssm(a);
     if (st != TTT_OK) return st;
     if (!prepare()) return TTT_ERR_CUDA;
-    return launched(launch_ssm_forward(a, static_cast<float*>(workspace), reinterpret_cast<cudaStream_t>(stream)), stream);
+    return launched(launch_ssm_forward(a, reinterpret_cast<cudaStream_t>(stream)), stream);
 }
 
 ttt_status ttt_ssm_decode(int B, int T, int C, int N, ttt_dtype dtype, int dt_softplus, long long ld_u,
@@ -314,7 +311,7 @@ ttt_status ttt_ssm_decode(int B, int T, int C, int N, ttt_dtype dtype, int dt_so
                           const float* D, const void* z, float* h, void* y, ttt_stream_t stream) {
     const SsmArgs a{B, T, C, N, dtype, dt_softplus, ld_u, ld_dt, ld_b, ld_c, ld_z, u, dt, dt_bias, A, Bm, Cm, D, z,
                     h, nullptr, y, h};
-    const ttt_status st = check_ssm(a, nullptr, 0, 0);
+    const ttt_status st = check_ssm(a);
     if (st != TTT_OK) return st;
     if (!prepare()) return TTT_ERR_CUDA;
     return launched(launch_ssm_token(a, reinterpret_cast<cudaStream_t>(stream)), stream);

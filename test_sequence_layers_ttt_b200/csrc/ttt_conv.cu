@@ -261,12 +261,13 @@ __global__ void __launch_bounds__(kThreads, 4) ttt_conv_backward_kernel(const Co
             for (int k = 0; k < P; k++) now[k] = zero2;
             if (kInside || t < live) {
                 float v[V];
-                f2 in[P], a[P];
+                f2 in[P];
                 row.get(v);
                 to_pairs<V>(v, in);
                 grad.get(v);
                 to_pairs<V>(v, now);
                 if constexpr (kSilu) {
+                    f2 a[P];
                     taps<W, P>(w, bias, win, in, a);
 #pragma unroll
                     for (int k = 0; k < P; k++) {  // dy s (1 + a (1 - s))

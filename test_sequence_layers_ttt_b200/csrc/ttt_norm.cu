@@ -94,7 +94,7 @@ struct NormParams {
 };
 
 template <typename T, int kNV, bool kShift, bool kQ8>
-__global__ void __launch_bounds__(512) ttt_rmsnorm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1) ttt_rmsnorm_kernel(const NormParams p) {
     constexpr int V = Elem<T>::kVec, P = V / 2;
     __shared__ float2 s[2][16];
     const long long group = (long long)blockIdx.x * blockDim.y + threadIdx.y;

@@ -116,9 +116,7 @@ cudaError_t launch_ssm_token(const SsmArgs& a, cudaStream_t stream) {
     return a.dtype == TTT_BF16 ? launch_token<__nv_bfloat16>(a, stream) : launch_token<float>(a, stream);
 }
 
-size_t ssm_forward_workspace_bytes(int, int, int, int) { return 0; }
-
-cudaError_t launch_ssm_forward(const SsmArgs& a, float*, cudaStream_t stream) {
+cudaError_t launch_ssm_forward(const SsmArgs& a, cudaStream_t stream) {
     // Blocks of 32 channels, one an SM.  Up to 37 of them (a quarter of 148 SMs) eight channels a block
     // still have an SM each, and those tiles, whose tokens are worked on side by side, take 61 clocks a
     // token against 87 (N = 16, bf16).  Above 16 states the warps of a block would hold too few registers

@@ -31,6 +31,7 @@ struct SsmBwdParams {
     float* ckpt;     // [B][chunks][4 kNW][C]
     float* part_bc;  // [cblocks][B][T][2][N]
     float* part_c;   // [B][N + 2][C]: dA, dD, ddt_bias
+    bool vec_rows, vec_bc;
 };
 
 // The block's 32 channels and sequence
@@ -57,7 +58,7 @@ struct CkptSmem {
 };
 
 // kK: tokens of a chunk; a tile is two chunks
-template <typename T, int kNW, int kK, bool kVecRows, bool kVecBC>
+template <typename T, int kNW, int kK>
 __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmBwdParams p) {
     constexpr int kNp = kStates * kNW, kTile = 2 * kK, kThreads = 32 * kNW;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -81,9 +82,9 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
     const auto stage = [&](int m) {
         RawTile<T, kTile, kNp>& r = s.raw[m & 1];
         const int t0 = m * kTile, width = p.C - w.c0;
-        stage_rows<T, kVecRows>(&r.u[0][0], static_cast<const T*>(p.u) + row0 * p.ld_u + w.c0, p.ld_u, t0, kTile, len, 32, width, tid, kThreads);
-        stage_rows<T, kVecRows>(&r.dt[0][0], static_cast<const T*>(p.dt) + row0 * p.ld_dt + w.c0, p.ld_dt, t0, kTile, len, 32, width, tid, kThreads);
-        stage_rows<T, kVecBC>(&r.b[0][0], static_cast<const T*>(p.Bm) + row0 * p.ld_b, p.ld_b, t0, kTile, len, kNp, p.N, tid, kThreads);
+        stage_rows<T>(p.vec_rows, &r.u[0][0], static_cast<const T*>(p.u) + row0 * p.ld_u + w.c0, p.ld_u, t0, kTile, len, 32, width, tid, kThreads);
+        stage_rows<T>(p.vec_rows, &r.dt[0][0], static_cast<const T*>(p.dt) + row0 * p.ld_dt + w.c0, p.ld_dt, t0, kTile, len, 32, width, tid, kThreads);
+        stage_rows<T>(p.vec_bc, &r.b[0][0], static_cast<const T*>(p.Bm) + row0 * p.ld_b, p.ld_b, t0, kTile, len, kNp, p.N, tid, kThreads);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (tiles > 0) stage(0);
@@ -180,7 +181,7 @@ struct BwdSmem {
 // where keeping the states there too left room for 256.
 constexpr int blocks_for(int kNW) { return kNW >= 8 ? 1 : 12 / kNW; }
 
-template <typename T, int kNW, int kK, bool kVecRows, bool kVecBC>
+template <typename T, int kNW, int kK>
 __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_kernel(const SsmBwdParams p) {
     constexpr int kNp = kStates * kNW, kQ = kK / 4, kThreads = 32 * kNW;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -219,13 +220,13 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
     const auto stage = [&](int chunk) {
         RawTile<T, kK, kNp>& r = s.raw[chunk & 1];
         const int t0 = chunk * kK, width = p.C - w.c0;
-        stage_rows<T, kVecRows>(&r.u[0][0], static_cast<const T*>(p.u) + row0 * p.ld_u + w.c0, p.ld_u, t0, kK, len, 32, width, tid, kThreads);
-        stage_rows<T, kVecRows>(&r.dt[0][0], static_cast<const T*>(p.dt) + row0 * p.ld_dt + w.c0, p.ld_dt, t0, kK, len, 32, width, tid, kThreads);
-        stage_rows<T, kVecRows>(&r.dy[0][0], static_cast<const T*>(p.dy) + row0 * p.C + w.c0, p.C, t0, kK, len, 32, width, tid, kThreads);
+        stage_rows<T>(p.vec_rows, &r.u[0][0], static_cast<const T*>(p.u) + row0 * p.ld_u + w.c0, p.ld_u, t0, kK, len, 32, width, tid, kThreads);
+        stage_rows<T>(p.vec_rows, &r.dt[0][0], static_cast<const T*>(p.dt) + row0 * p.ld_dt + w.c0, p.ld_dt, t0, kK, len, 32, width, tid, kThreads);
+        stage_rows<T>(p.vec_rows, &r.dy[0][0], static_cast<const T*>(p.dy) + row0 * p.C + w.c0, p.C, t0, kK, len, 32, width, tid, kThreads);
         if (p.z)
-            stage_rows<T, kVecRows>(&r.z[0][0], static_cast<const T*>(p.z) + row0 * p.ld_z + w.c0, p.ld_z, t0, kK, len, 32, width, tid, kThreads);
-        stage_rows<T, kVecBC>(&r.b[0][0], static_cast<const T*>(p.Bm) + row0 * p.ld_b, p.ld_b, t0, kK, len, kNp, p.N, tid, kThreads);
-        stage_rows<T, kVecBC>(&r.c[0][0], static_cast<const T*>(p.Cm) + row0 * p.ld_c, p.ld_c, t0, kK, len, kNp, p.N, tid, kThreads);
+            stage_rows<T>(p.vec_rows, &r.z[0][0], static_cast<const T*>(p.z) + row0 * p.ld_z + w.c0, p.ld_z, t0, kK, len, 32, width, tid, kThreads);
+        stage_rows<T>(p.vec_bc, &r.b[0][0], static_cast<const T*>(p.Bm) + row0 * p.ld_b, p.ld_b, t0, kK, len, kNp, p.N, tid, kThreads);
+        stage_rows<T>(p.vec_bc, &r.c[0][0], static_cast<const T*>(p.Cm) + row0 * p.ld_c, p.ld_c, t0, kK, len, kNp, p.N, tid, kThreads);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const auto load_first = [&](int chunk) {
@@ -466,12 +467,12 @@ Layout layout(int B, int T, int C, int N) {
     return l;
 }
 
-template <typename T, int kNW, bool kVecRows, bool kVecBC>
+template <typename T, int kNW>
 cudaError_t launch(const SsmBwdParams& p, cudaStream_t stream) {
     constexpr int kK = chunk_for(kNW);
     const unsigned grid = (unsigned)((long long)p.B * p.cblocks);
-    const auto first = ttt_ssm_checkpoint_kernel<T, kNW, kK, kVecRows, kVecBC>;
-    const auto second = ttt_ssm_backward_kernel<T, kNW, kK, kVecRows, kVecBC>;
+    const auto first = ttt_ssm_checkpoint_kernel<T, kNW, kK>;
+    const auto second = ttt_ssm_backward_kernel<T, kNW, kK>;
     constexpr int smem1 = (int)sizeof(CkptSmem<T, kNW, 2 * kK>), smem2 = (int)sizeof(BwdSmem<T, kNW, kK>);
     static_assert(smem1 <= (int)kMaxSmem && smem2 <= (int)kMaxSmem, "fits an SM");
     cudaError_t e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
@@ -484,26 +485,14 @@ cudaError_t launch(const SsmBwdParams& p, cudaStream_t stream) {
     return cudaPeekAtLastError();
 }
 
-template <typename T, int kNW>
-cudaError_t by_alignment(const SsmBwdParams& p, cudaStream_t stream) {
-    constexpr int es = sizeof(T);
-    const bool rows = rows16(p.u, p.ld_u, p.C, es) && rows16(p.dt, p.ld_dt, p.C, es) && rows16(p.z, p.ld_z, p.C, es) &&
-                      rows16(p.dy, p.C, p.C, es);
-    const bool bc = rows16(p.Bm, p.ld_b, p.N, es) && rows16(p.Cm, p.ld_c, p.N, es);
-    if constexpr (kNW * kStates * es >= 16)  // else a row of B is no whole unit at any N
-        if (rows && bc) return launch<T, kNW, true, true>(p, stream);
-    if (rows) return launch<T, kNW, true, false>(p, stream);
-    return launch<T, kNW, false, false>(p, stream);
-}
-
 template <typename T>
 cudaError_t dispatch(const SsmBwdParams& p, cudaStream_t stream) {
     switch (warps_for(p.N)) {
-        case 1: return by_alignment<T, 1>(p, stream);
-        case 2: return by_alignment<T, 2>(p, stream);
-        case 4: return by_alignment<T, 4>(p, stream);
-        case 8: return by_alignment<T, 8>(p, stream);
-        default: return by_alignment<T, 16>(p, stream);
+        case 1: return launch<T, 1>(p, stream);
+        case 2: return launch<T, 2>(p, stream);
+        case 4: return launch<T, 4>(p, stream);
+        case 8: return launch<T, 8>(p, stream);
+        default: return launch<T, 16>(p, stream);
     }
 }
 
@@ -551,6 +540,10 @@ cudaError_t launch_ssm_backward(const SsmBwdArgs& a, float* workspace, cudaStrea
     p.ckpt = workspace;
     p.part_bc = workspace + l.ckpt;
     p.part_c = p.part_bc + l.part_bc;
+    const int es = f.dtype == TTT_BF16 ? 2 : 4;
+    p.vec_rows = rows16(f.u, f.ld_u, f.C, es) && rows16(f.dt, f.ld_dt, f.C, es) && rows16(f.z, f.ld_z, f.C, es) &&
+                 rows16(a.dy, f.C, f.C, es);
+    p.vec_bc = rows16(f.Bm, f.ld_b, f.N, es) && rows16(f.Cm, f.ld_c, f.N, es);
     cudaError_t e = f.dtype == TTT_BF16 ? dispatch<__nv_bfloat16>(p, stream) : dispatch<float>(p, stream);
     if (e != cudaSuccess) return e;
     const size_t bc = (size_t)f.B * f.T * 2 * f.N;

@@ -50,7 +50,7 @@ struct ScanSmem {
     }
 };
 
-template <typename T, int kWarps, bool kVecRows, bool kVecBC>
+template <typename T, int kWarps>
 __global__ void __launch_bounds__(32 * (kWarps + kHelpers)) ttt_ssm_scan_kernel(const Params p, const int cblocks) {
     using Smem = ScanSmem<T>;
     constexpr int kTile = Smem::kTile, kQuads = Smem::kQuads, kPitch = Smem::kPitch, kNp = kWarps * kStates;
@@ -72,11 +72,11 @@ __global__ void __launch_bounds__(32 * (kWarps + kHelpers)) ttt_ssm_scan_kernel(
     // raw rows of tile m on their way
     const auto stage = [&](int m) {
         const int t0 = m * kTile, buf = m & 3, width = p.C - c0;
-        stage_rows<T, kVecRows>(s.u + buf * kTile * 32, u_rows, p.ld_u, t0, kTile, len, 32, width, hid, 32 * kHelpers);
-        stage_rows<T, kVecRows>(s.raw + buf * kTile * 32, dt_rows, p.ld_dt, t0, kTile, len, 32, width, hid, 32 * kHelpers);
-        if (p.z) stage_rows<T, kVecRows>(s.z + buf * kTile * 32, z_rows, p.ld_z, t0, kTile, len, 32, width, hid, 32 * kHelpers);
-        stage_rows<T, kVecBC>(s.rb + buf * kTile * kNp, b_rows, p.ld_b, t0, kTile, len, kNp, p.N, hid, 32 * kHelpers);
-        stage_rows<T, kVecBC>(s.rc + buf * kTile * kNp, c_rows, p.ld_c, t0, kTile, len, kNp, p.N, hid, 32 * kHelpers);
+        stage_rows<T>(p.vec_rows, s.u + buf * kTile * 32, u_rows, p.ld_u, t0, kTile, len, 32, width, hid, 32 * kHelpers);
+        stage_rows<T>(p.vec_rows, s.raw + buf * kTile * 32, dt_rows, p.ld_dt, t0, kTile, len, 32, width, hid, 32 * kHelpers);
+        if (p.z) stage_rows<T>(p.vec_rows, s.z + buf * kTile * 32, z_rows, p.ld_z, t0, kTile, len, 32, width, hid, 32 * kHelpers);
+        stage_rows<T>(p.vec_bc, s.rb + buf * kTile * kNp, b_rows, p.ld_b, t0, kTile, len, kNp, p.N, hid, 32 * kHelpers);
+        stage_rows<T>(p.vec_bc, s.rc + buf * kTile * kNp, c_rows, p.ld_c, t0, kTile, len, kNp, p.N, hid, 32 * kHelpers);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f, skip = on && p.D ? p.D[c] : 0.f;
@@ -216,23 +216,15 @@ __global__ void __launch_bounds__(32 * (kWarps + kHelpers)) ttt_ssm_scan_kernel(
 template <typename T, int kWarps>
 cudaError_t launch(const SsmArgs& a, cudaStream_t stream) {
     const Params p = params_of(a);
-    constexpr int es = sizeof(T);
     const long long cblocks = (a.C + 31) / 32, grid = a.B * cblocks;
     if (grid >= (1LL << 31)) return cudaErrorInvalidValue;
-    const bool rows = rows16(a.u, a.ld_u, a.C, es) && rows16(a.dt, a.ld_dt, a.C, es) && rows16(a.z, a.ld_z, a.C, es);
-    const bool bc = rows16(a.Bm, a.ld_b, a.N, es) && rows16(a.Cm, a.ld_c, a.N, es);
     const size_t smem = ScanSmem<T>::bytes(kWarps, kWarps * kStates);
     static_assert(ScanSmem<T>::bytes(4, 16) <= kMaxSmem, "fits an SM");
-    const auto run = [&](auto kernel) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)grid, 32 * (kWarps + kHelpers), smem, stream>>>(p, (int)cblocks);
-        return cudaPeekAtLastError();
-    };
-    if constexpr (kWarps * kStates * es >= 16)  // else a row of B is no whole unit at any N
-        if (rows && bc) return run(ttt_ssm_scan_kernel<T, kWarps, true, true>);
-    if (rows) return run(ttt_ssm_scan_kernel<T, kWarps, true, false>);
-    return run(ttt_ssm_scan_kernel<T, kWarps, false, false>);
+    const auto kernel = ttt_ssm_scan_kernel<T, kWarps>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)grid, 32 * (kWarps + kHelpers), smem, stream>>>(p, (int)cblocks);
+    return cudaPeekAtLastError();
 }
 
 template <typename T>

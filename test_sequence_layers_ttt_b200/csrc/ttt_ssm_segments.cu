@@ -49,7 +49,7 @@ struct SegSmem {
     }
 };
 
-template <typename T, int kL, bool kVecRows, bool kVecBC>
+template <typename T, int kL>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(const Params p, const int cblocks, const int n_pad) {
     constexpr int kQ = 32 / kL;
     constexpr int kOwn = kSeg / kQ;  // tokens whose elementwise work a lane does
@@ -70,11 +70,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
 
     const auto stage = [&](int t0, int buf) {
         const int width = p.C - c0;
-        stage_rows<T, kVecRows>(s.u + buf * tile * kL, u_rows, p.ld_u, t0, tile, len, kL, width, tid, threads);
-        stage_rows<T, kVecRows>(s.dt + buf * tile * kL, dt_rows, p.ld_dt, t0, tile, len, kL, width, tid, threads);
-        if (p.z) stage_rows<T, kVecRows>(s.z + buf * tile * kL, z_rows, p.ld_z, t0, tile, len, kL, width, tid, threads);
-        stage_rows<T, kVecBC>(s.rb + buf * tile * n_pad, b_rows, p.ld_b, t0, tile, len, n_pad, p.N, tid, threads);
-        stage_rows<T, kVecBC>(s.rc + buf * tile * n_pad, c_rows, p.ld_c, t0, tile, len, n_pad, p.N, tid, threads);
+        stage_rows<T>(p.vec_rows, s.u + buf * tile * kL, u_rows, p.ld_u, t0, tile, len, kL, width, tid, threads);
+        stage_rows<T>(p.vec_rows, s.dt + buf * tile * kL, dt_rows, p.ld_dt, t0, tile, len, kL, width, tid, threads);
+        if (p.z) stage_rows<T>(p.vec_rows, s.z + buf * tile * kL, z_rows, p.ld_z, t0, tile, len, kL, width, tid, threads);
+        stage_rows<T>(p.vec_bc, s.rb + buf * tile * n_pad, b_rows, p.ld_b, t0, tile, len, n_pad, p.N, tid, threads);
+        stage_rows<T>(p.vec_bc, s.rc + buf * tile * n_pad, c_rows, p.ld_c, t0, tile, len, n_pad, p.N, tid, threads);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
 template <typename T, int kL>
 cudaError_t launch(const SsmArgs& a, cudaStream_t stream) {
     const Params p = params_of(a);
-    constexpr int es = sizeof(T), step = kStates * (32 / kL);
+    constexpr int step = kStates * (32 / kL);
     int n_pad = step;
     while (n_pad < a.N) n_pad *= 2;
     const long long cblocks = (a.C + kL - 1) / kL, grid = a.B * cblocks;
@@ -264,18 +264,12 @@ cudaError_t launch(const SsmArgs& a, cudaStream_t stream) {
     const int segs = (a.T + kSeg - 1) / kSeg;
     int warps = segs < 1 ? 1 : (segs < kMaxWarps ? segs : kMaxWarps);
     while (warps > 1 && SegSmem<T, kL>::bytes(kSeg * warps, n_pad) > kMaxSmem) warps--;
-    const bool rows = rows16(a.u, a.ld_u, a.C, es) && rows16(a.dt, a.ld_dt, a.C, es) && rows16(a.z, a.ld_z, a.C, es);
-    const bool bc = rows16(a.Bm, a.ld_b, a.N, es) && rows16(a.Cm, a.ld_c, a.N, es);
     const size_t smem = SegSmem<T, kL>::bytes(kSeg * warps, n_pad);
-    const auto run = [&](auto kernel) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        kernel<<<(unsigned)grid, 32 * warps, smem, stream>>>(p, (int)cblocks, n_pad);
-        return cudaPeekAtLastError();
-    };
-    if (rows && bc) return run(ttt_ssm_segments_kernel<T, kL, true, true>);
-    if (rows) return run(ttt_ssm_segments_kernel<T, kL, true, false>);
-    return run(ttt_ssm_segments_kernel<T, kL, false, false>);
+    const auto kernel = ttt_ssm_segments_kernel<T, kL>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)grid, 32 * warps, smem, stream>>>(p, (int)cblocks, n_pad);
+    return cudaPeekAtLastError();
 }
 
 }  // namespace

@@ -105,9 +105,8 @@ def test_conv_aliases_and_workspace():
 
 
 # ---------------------------------------------------------------- scan
-def ssm(B=2, T=5, C=8, N=4, dtype=0, lds=None, ws=1 << 40, **at):
-    # u dt dt_bias A B C D z h0 lengths y h_T workspace
-    return b.lib.ttt_ssm_forward(B, T, C, N, dtype, 1, *(lds or (C, C, N, N, C)), *fake(13, **at), ws, None)
+def ssm(B=2, T=5, C=8, N=4, dtype=0, lds=None, **at):  # u dt dt_bias A B C D z h0 lengths y h_T
+    return b.lib.ttt_ssm_forward(B, T, C, N, dtype, 1, *(lds or (C, C, N, N, C)), *fake(12, **at), None)
 
 
 def ssm_dec(B=2, T=1, C=8, N=4, dtype=0, lds=None, **at):  # u dt dt_bias A B C D z h y
@@ -121,7 +120,7 @@ def ssm_bwd(B=2, T=5, C=8, N=4, dtype=0, lds=None, ws=1 << 40, **at):
 
 @pytest.mark.parametrize("call", [ssm, ssm_dec, ssm_bwd])
 @pytest.mark.parametrize("kw,code", [
-    (dict(B=0), SHAPE), (dict(T=-1), SHAPE), (dict(C=0), SHAPE), (dict(N=0), SHAPE), (dict(N=65), UNSUP),
+    (dict(B=0), SHAPE), (dict(B=1, T=(1 << 31) - (1 << 16)), SHAPE), (dict(T=-1), SHAPE), (dict(C=0), SHAPE), (dict(N=0), SHAPE), (dict(N=65), UNSUP),
     (dict(dtype=9), DTYPE), (dict(lds=(7, 8, 4, 4, 8)), SHAPE), (dict(lds=(8, 8, 3, 4, 8)), SHAPE),
     (dict(lds=(8, 8, 4, 4, 7)), SHAPE), (dict(p0=None), NULL), (dict(p3=None), NULL), (dict(p5=None), NULL),
     (dict(p0=BASE + 1), ALIGN), (dict(p3=BASE + 3 * STRIDE + 4), ALIGN),
@@ -145,7 +144,6 @@ def test_ssm_aliases_and_workspace():
 def test_workspace_queries_of_bad_shapes_are_zero():
     assert b.lib.ttt_ssm_backward_workspace_size(0, 5, 8, 4) == 0
     assert b.lib.ttt_ssm_backward_workspace_size(1, 5, 8, 65) == 0
-    assert b.lib.ttt_ssm_forward_workspace_size(1, -1, 8, 4) == 0
     assert b.lib.ttt_conv_backward_workspace_size(1, 5, 8, 9) == 0
     assert b.lib.ttt_rmsnorm_backward_workspace_size(1, 1, 20000, 0) == 0
 
