@@ -500,7 +500,7 @@ class _Launch:
     def __enter__(self):
         dev = self.dev
         self.entered = ()
-        if dev.index != torch.cuda.current_device():
+        if dev.index != torch._C._cuda_getDevice():
             self.entered = (torch.cuda.device(dev),)
         if self.stream is not None:
             self.entered += (torch.cuda.stream(_launch_stream(dev, self.stream)),)
@@ -538,6 +538,14 @@ def _dense(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> Optional[
     if t.shape != shape or t.dtype != dtype or t.get_device() != dev.index or not t.is_contiguous():
         _refuse(t, name, shape, dtype, dev, "a contiguous CUDA tensor")
     return t.data_ptr()
+
+
+def _out(t: Optional[torch.Tensor], name: str, like: torch.Tensor, shape, dtype, dev):
+    """An output and its address: the caller's tensor, checked, or a new one."""
+    if t is None:
+        t = like.new_empty(shape) if dtype is like.dtype else torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _dense(t, name, shape, dtype, dev)
 
 
 def _rows(t: Optional[torch.Tensor], name: str, shape, dtype, dev):
@@ -580,10 +588,11 @@ def ttt_rmsnorm_forward(x, weight, residual=None, *, eps: float = 1e-6, y=None, 
     px, pr = _dense(x, "x", (B, T, d), dt, dev), _dense(residual, "residual", (B, T, d), dt, dev)
     pw = _dense(weight, "weight", (d,), torch.float32, dev)
     with _Launch(dev, stream) as s:
-        y = torch.empty_like(x) if y is None else y
-        h = torch.empty_like(x) if h is None and residual is not None else h
-        _check(lib.ttt_rmsnorm_forward(B, T, d, code, eps, px, pr, pw, _dense(y, "y", (B, T, d), dt, dev),
-                                       _dense(h, "h", (B, T, d), dt, dev), s))
+        y, py = _out(y, "y", x, (B, T, d), dt, dev)
+        ph = None
+        if h is not None or residual is not None:
+            h, ph = _out(h, "h", x, (B, T, d), dt, dev)
+        _check(lib.ttt_rmsnorm_forward(B, T, d, code, eps, px, pr, pw, py, ph, s))
     return y, h
 
 
@@ -596,13 +605,12 @@ def ttt_rmsnorm_q8_forward(x, weight, residual=None, *, eps: float = 1e-6, q=Non
     px, pr = _dense(x, "x", (B, T, d), dt, dev), _dense(residual, "residual", (B, T, d), dt, dev)
     pw = _dense(weight, "weight", (d,), torch.float32, dev)
     with _Launch(dev, stream) as s:
-        q = torch.empty((B, T, d), dtype=torch.float8_e4m3fn, device=dev) if q is None else q
-        scale = torch.empty((B, T), dtype=torch.float32, device=dev) if scale is None else scale
-        h = torch.empty_like(x) if h is None and residual is not None else h
-        _check(lib.ttt_rmsnorm_q8_forward(B, T, d, code, eps, px, pr, pw,
-                                          _dense(q, "q", (B, T, d), torch.float8_e4m3fn, dev),
-                                          _dense(scale, "scale", (B, T), torch.float32, dev),
-                                          _dense(h, "h", (B, T, d), dt, dev), s))
+        q, pq = _out(q, "q", x, (B, T, d), torch.float8_e4m3fn, dev)
+        scale, ps = _out(scale, "scale", weight, (B, T), torch.float32, dev)
+        ph = None
+        if h is not None or residual is not None:
+            h, ph = _out(h, "h", x, (B, T, d), dt, dev)
+        _check(lib.ttt_rmsnorm_q8_forward(B, T, d, code, eps, px, pr, pw, pq, ps, ph, s))
     return q, scale, h
 
 
@@ -689,11 +697,9 @@ def ttt_conv_forward(x, weight, bias=None, state0=None, *, lengths=None, activat
     B, T, C, W, _ = shape
     dev, dt = x.device, x.dtype
     with _Launch(dev, stream) as s:
-        y = x.new_empty((B, T, C)) if y is None else y
-        state_T = torch.empty((B, W - 1, C), dtype=dt, device=dev) if state_T is None else state_T
-        _check(lib.ttt_conv_forward(*shape, _silu_code(activation), ld, px, pw, pb, ps, pl,
-                                    _dense(y, "y", (B, T, C), dt, dev),
-                                    _dense(state_T, "state_T", (B, W - 1, C), dt, dev), s))
+        y, py = _out(y, "y", x, (B, T, C), dt, dev)
+        state_T, pt = _out(state_T, "state_T", x, (B, W - 1, C), dt, dev)
+        _check(lib.ttt_conv_forward(*shape, _silu_code(activation), ld, px, pw, pb, ps, pl, py, pt, s))
     return y, state_T
 
 
@@ -706,9 +712,8 @@ def ttt_conv_decode(x, weight, bias, state, *, activation="silu", y=None, stream
     B, T, C, W, _ = shape
     dev, dt = x.device, x.dtype
     with _Launch(dev, stream) as s:
-        y = x.new_empty((B, T, C)) if y is None else y
-        _check(lib.ttt_conv_decode(*shape, _silu_code(activation), ld, px, pw, pb, ps,
-                                   _dense(y, "y", (B, T, C), dt, dev), s))
+        y, py = _out(y, "y", x, (B, T, C), dt, dev)
+        _check(lib.ttt_conv_decode(*shape, _silu_code(activation), ld, px, pw, pb, ps, py, s))
     return y
 
 
@@ -758,10 +763,9 @@ def ttt_ssm_forward(u, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, 
     B, T, C, N, _ = shape
     dev = u.device
     with _Launch(dev, stream) as s:
-        y = u.new_empty((B, T, C)) if y is None else y
-        h_T = torch.empty((B, C, N), dtype=torch.float32, device=dev) if h_T is None else h_T
-        _check(lib.ttt_ssm_forward(*shape, int(bool(dt_softplus)), *lds, *ptrs, _dense(y, "y", (B, T, C), u.dtype, dev),
-                                   _dense(h_T, "h_T", (B, C, N), torch.float32, dev), s))
+        y, py = _out(y, "y", u, (B, T, C), u.dtype, dev)
+        h_T, ph = _out(h_T, "h_T", A, (B, C, N), torch.float32, dev)
+        _check(lib.ttt_ssm_forward(*shape, int(bool(dt_softplus)), *lds, *ptrs, py, ph, s))
     return y, h_T
 
 
@@ -773,9 +777,8 @@ def ttt_ssm_decode(u, dt, A, Bm, Cm, h, D=None, z=None, dt_bias=None, *, dt_soft
     B, T, C, N, _ = shape
     dev = u.device
     with _Launch(dev, stream) as s:
-        y = u.new_empty((B, T, C)) if y is None else y
-        _check(lib.ttt_ssm_decode(*shape, int(bool(dt_softplus)), *lds, *ptrs[:-1],
-                                  _dense(y, "y", (B, T, C), u.dtype, dev), s))
+        y, py = _out(y, "y", u, (B, T, C), u.dtype, dev)
+        _check(lib.ttt_ssm_decode(*shape, int(bool(dt_softplus)), *lds, *ptrs[:-1], py, s))
     return y
 
 
