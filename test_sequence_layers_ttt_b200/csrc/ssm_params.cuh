@@ -86,7 +86,19 @@ __device__ __forceinline__ void stage_rows_by(T* dst, const T* src, long long ld
         T* to = dst + r * cols + c;
         const long long advance = step * ld;
         const int last = c < width ? len - t0 : 0;
-        for (; r < rows; r += step, from += advance, to += step * cols) put(to, r < last ? from : src, r < last);
+        if constexpr (kVec || sizeof(T) == 4) {
+            for (; r < rows; r += step, from += advance, to += step * cols) put(to, r < last ? from : src, r < last);
+        } else {
+            // there is no asynchronous copy of two bytes: eight loads on their way before the first is stored
+            for (; r < rows; r += 8 * step, from += 8 * advance, to += 8 * step * cols) {
+                T v[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++) v[k] = r + k * step < last ? from[k * advance] : T(0.f);
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    if (r + k * step < rows) to[k * step * cols] = v[k];
+            }
+        }
     } else {
         for (int i = tid; i < rows * per; i += threads) {
             const int r = i >> shift, c = (i & (per - 1)) * kV;

@@ -12,7 +12,19 @@
 // of one, so that B and C are one broadcast read each; the warps of a block share out the states.  Sums
 // over states meet in shared memory, sums over the block's channels in shuffles; what is summed over
 // blocks or sequences goes through the workspace and is added up in an order that the shape fixes.
+// Where B and the channels make few blocks, the time axis is split too (split_of): one more pass takes each part
+// for itself and leaves its end state, its gradient to the part before and its decay, from which the blocks of
+// the two passes above fold the state and the gradient that they start from.
+//
+// Sums over tokens are of chunks' sums in fp32, added in 64 bits.  What is left of dA's error (4e-7 to 9e-7 of its
+// norm over thousands of tokens) is the decays' rounding to fp32, which alone gives 4e-7 to 7e-7.
+//
+// Measured (8 x 2048 x 1536, 16 states, bf16): 1.00 ms, the second pass 0.79 and the first 0.21, of which HBM would take
+// 0.05 and the special functions 0.17.  The second pass issues in 56 % of the clocks and keeps the shared
+// memory pipe 60 % busy, most of it the shuffles and the states' way through shared memory.
 #include "ssm_params.cuh"
+
+#include <algorithm>
 
 namespace ttt {
 namespace {
@@ -21,6 +33,7 @@ using namespace ssm;
 
 struct SsmBwdParams {
     int B, T, C, N, chunks, cblocks;
+    int segs, seg_len;  // parts of the time axis and their tokens
     long long ld_u, ld_dt, ld_b, ld_c, ld_z;
     int softplus;
     const void *u, *dt, *Bm, *Cm, *z, *dy;
@@ -30,16 +43,57 @@ struct SsmBwdParams {
     float* dh0;
     float* ckpt;     // [B][chunks][4 kNW][C]
     float* part_bc;  // [cblocks][B][T][2][N]
-    float* part_c;   // [B][N + 2][C]: dA, dD, ddt_bias
+    float* part_c;   // [B][segs][N + 2][C]: dA, dD, ddt_bias
+    float* carry;    // [B][segs][3][4 kNW][C]: a part's end state from zero, its gradient to the part before, its decay
     bool vec_rows, vec_bc;
 };
 
-// The block's 32 channels and sequence
+// The block's 32 channels and its part of a sequence: tokens t0 .. t0 + T, the first len of them no padding
 struct Where {
-    int b, c0;
+    int b, seg, cblk, c0, t0, T, len;
 };
-__device__ __forceinline__ Where where(int cblocks) {
-    return {(int)(blockIdx.x / cblocks), (int)(blockIdx.x % cblocks) * 32};
+__device__ __forceinline__ Where where(const SsmBwdParams& p) {
+    Where w;
+    const int row = (int)(blockIdx.x / p.cblocks);
+    w.cblk = (int)(blockIdx.x % p.cblocks);
+    w.c0 = w.cblk * 32;
+    w.b = row / p.segs;
+    w.seg = row % p.segs;
+    w.t0 = w.seg * p.seg_len;
+    w.T = min(p.T - w.t0, p.seg_len);
+    w.len = max(min(length_of(p.lengths, w.b, p.T) - w.t0, w.T), 0);
+    return w;
+}
+// Carry value m (0: state, 1: gradient, 2: decay) of part seg, of the thread's first state n0 and channel c
+template <int kNp>
+__device__ __forceinline__ size_t carry_at(const SsmBwdParams& p, int b, int seg, int m, int n0, int c) {
+    return ((((size_t)b * p.segs + seg) * 3 + m) * kNp + n0) * p.C + c;
+}
+// a v + e; 0 becomes e where the decay of a whole part, of a growing state, has overflowed
+__device__ __forceinline__ float carried(float v, float a, float e) { return v == 0.f ? e : fmaf(a, v, e); }
+// v folded over `count` parts from part `from` on, in steps of `by`; m as in carry_at.  Eight parts' values are on
+// their way at a time: one by one, 64 parts took longer than a walk along one of them.
+template <int kNp>
+__device__ __forceinline__ void fold(float (&v)[kStates], const SsmBwdParams& p, int b, int from, int by, int count, int m,
+                                     int n0, int c) {
+    for (int j0 = 0; j0 < count; j0 += 8) {
+        float e[8][kStates], a[8][kStates];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const bool live = j0 + j < count;
+            const int seg = live ? from + (j0 + j) * by : 0;
+            const float *pe = p.carry + carry_at<kNp>(p, b, seg, m, n0, c), *pa = p.carry + carry_at<kNp>(p, b, seg, 2, n0, c);
+#pragma unroll
+            for (int i = 0; i < kStates; i++) {
+                e[j][i] = live ? pe[(size_t)i * p.C] : 0.f;
+                a[j][i] = live ? pa[(size_t)i * p.C] : 1.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+            for (int i = 0; i < kStates; i++) v[i] = carried(v[i], a[j][i], e[j][i]);
+    }
 }
 
 // Rows of a tile of kK tokens as they come from memory
@@ -50,41 +104,52 @@ struct RawTile {
 };
 
 // ---------------------------------------------------------------- pass 1: the states at the chunks' starts
-template <typename T, int kNW, int kTile>
+template <typename T, int kNW, int kTile, bool kEnds>
 struct CkptSmem {
     RawTile<T, kTile, kStates * kNW> raw[2];
-    float4 dt[kTile / 4][32], du[kTile / 4][32];
-    float b[kStates * kNW][kTile + 4];
+    float4 dt[kTile / 4][32], du[kTile / 4][32], dy[kEnds ? kTile / 4 : 1][32];
+    float b[kStates * kNW][kTile + 4], c[kEnds ? kStates * kNW : 1][kTile + 4];
 };
 
-// kK: tokens of a chunk; a tile is two chunks
-template <typename T, int kNW, int kK>
+// kK: tokens of a chunk; a tile is two chunks.  kEnds: a part of the time axis for itself, as carry has it.
+// The gradient that leaves a part to the one before is sum_t (a_first ... a_t) C_t dy'_t, so it too is
+// summed walking forwards.
+template <typename T, int kNW, int kK, bool kEnds>
 __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmBwdParams p) {
     constexpr int kNp = kStates * kNW, kTile = 2 * kK, kThreads = 32 * kNW;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    CkptSmem<T, kNW, kTile>& s = *reinterpret_cast<CkptSmem<T, kNW, kTile>*>(smem_raw);
+    CkptSmem<T, kNW, kTile, kEnds>& s = *reinterpret_cast<CkptSmem<T, kNW, kTile, kEnds>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Where w = where(p.cblocks);
+    const Where w = where(p);
     const int c = w.c0 + lane;
     const bool on = c < p.C;
-    const int len = length_of(p.lengths, w.b, p.T);
+    const int len = w.len;
     const int n_chunks = (len + kK - 1) / kK, tiles = (len + kTile - 1) / kTile;
     const int n0 = warp * kStates;
-    float h[kStates], a2[kStates];
+    float h[kStates], a2[kStates], back[kStates], all[kStates];
 #pragma unroll
     for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N;
         a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
-        h[i] = live && p.h0 ? p.h0[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
+        h[i] = !kEnds && live && p.h0 ? p.h0[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
+        back[i] = 0.f;
+        all[i] = 1.f;
     }
+    if (!kEnds && on) fold<kNp>(h, p, w.b, 0, 1, w.seg, 0, n0, c);
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f;
-    const long long row0 = (long long)w.b * p.T;
+    const long long row0 = (long long)w.b * p.T + w.t0;
     const auto stage = [&](int m) {
         RawTile<T, kTile, kNp>& r = s.raw[m & 1];
         const int t0 = m * kTile, width = p.C - w.c0;
         stage_rows<T>(p.vec_rows, &r.u[0][0], static_cast<const T*>(p.u) + row0 * p.ld_u + w.c0, p.ld_u, t0, kTile, len, 32, width, tid, kThreads);
         stage_rows<T>(p.vec_rows, &r.dt[0][0], static_cast<const T*>(p.dt) + row0 * p.ld_dt + w.c0, p.ld_dt, t0, kTile, len, 32, width, tid, kThreads);
         stage_rows<T>(p.vec_bc, &r.b[0][0], static_cast<const T*>(p.Bm) + row0 * p.ld_b, p.ld_b, t0, kTile, len, kNp, p.N, tid, kThreads);
+        if (kEnds) {
+            stage_rows<T>(p.vec_rows, &r.dy[0][0], static_cast<const T*>(p.dy) + row0 * p.C + w.c0, p.C, t0, kTile, len, 32, width, tid, kThreads);
+            if (p.z)
+                stage_rows<T>(p.vec_rows, &r.z[0][0], static_cast<const T*>(p.z) + row0 * p.ld_z + w.c0, p.ld_z, t0, kTile, len, 32, width, tid, kThreads);
+            stage_rows<T>(p.vec_bc, &r.c[0][0], static_cast<const T*>(p.Cm) + row0 * p.ld_c, p.ld_c, t0, kTile, len, kNp, p.N, tid, kThreads);
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     if (tiles > 0) stage(0);
@@ -103,19 +168,34 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
             }
             s.dt[q][lane] = make_float4(dt[0], dt[1], dt[2], dt[3]);
             s.du[q][lane] = make_float4(du[0], du[1], du[2], du[3]);
+            if constexpr (kEnds) {
+                float dy[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    dy[k] = to_f32(r.dy[4 * q + k][lane]);
+                    if (p.z) {
+                        const float z = to_f32(r.z[4 * q + k][lane]);
+                        dy[k] *= z * sigmoid(z);
+                    }
+                }
+                s.dy[q][lane] = make_float4(dy[0], dy[1], dy[2], dy[3]);
+            }
         }
-        for (int i = tid; i < kTile * kNp; i += kThreads) s.b[i % kNp][i / kNp] = to_f32(r.b[i / kNp][i % kNp]);
+        for (int i = tid; i < kTile * kNp; i += kThreads) {
+            s.b[i % kNp][i / kNp] = to_f32(r.b[i / kNp][i % kNp]);
+            if constexpr (kEnds) s.c[i % kNp][i / kNp] = to_f32(r.c[i / kNp][i % kNp]);
+        }
         __syncthreads();
 #pragma unroll
         for (int half = 0; half < 2; half++) {
             const int chunk = 2 * m + half;
-            if (on && chunk < n_chunks) {
-                float* out = p.ckpt + (((size_t)w.b * p.chunks + chunk) * kNp + n0) * p.C + c;
+            if (!kEnds && on && chunk < n_chunks) {
+                float* out = p.ckpt + (((size_t)w.b * p.chunks + w.t0 / kK + chunk) * kNp + n0) * p.C + c;
 #pragma unroll
                 for (int i = 0; i < kStates; i++) out[(size_t)i * p.C] = h[i];
             }
             constexpr int kQ = kK / 4;
-            f2 dt[2 * kQ], du[2 * kQ];
+            f2 dt[2 * kQ], du[2 * kQ], dy[2 * kQ];
 #pragma unroll
             for (int q = 0; q < kQ; q++) {
                 const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s.dt[half * kQ + q][lane]);
@@ -124,6 +204,11 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
                 dt[2 * q + 1] = d.y;
                 du[2 * q] = e.x;
                 du[2 * q + 1] = e.y;
+                if constexpr (kEnds) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&s.dy[half * kQ + q][lane]);
+                    dy[2 * q] = f.x;
+                    dy[2 * q + 1] = f.y;
+                }
             }
 #pragma unroll
             for (int i = 0; i < kStates; i++) {
@@ -144,8 +229,27 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
                     h[i] = fmaf(a[4 * q + 1], h[i], v1);
                     h[i] = fmaf(a[4 * q + 2], h[i], v2);
                     h[i] = fmaf(a[4 * q + 3], h[i], v3);
+                    if constexpr (kEnds) {
+                        const ulonglong2 Cq = reinterpret_cast<const ulonglong2*>(&s.c[n0 + i][half * kK])[q];
+                        float g[4];
+                        unpack2(mul2(dy[2 * q], Cq.x), g[0], g[1]);
+                        unpack2(mul2(dy[2 * q + 1], Cq.y), g[2], g[3]);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            all[i] *= a[4 * q + k];
+                            back[i] = carried(g[k], all[i], back[i]);
+                        }
+                    }
                 }
             }
+        }
+    }
+    if (kEnds && on) {
+#pragma unroll
+        for (int i = 0; i < kStates; i++) {
+            p.carry[carry_at<kNp>(p, w.b, w.seg, 0, n0 + i, c)] = h[i];
+            p.carry[carry_at<kNp>(p, w.b, w.seg, 1, n0 + i, c)] = back[i];
+            p.carry[carry_at<kNp>(p, w.b, w.seg, 2, n0 + i, c)] = all[i];
         }
     }
 }
@@ -175,7 +279,9 @@ struct BwdSmem {
     // a thread's states after each token, four tokens of a state together; once a quad has been walked back, its
     // first three places hold the thread's parts of g . B, of the sum with A, and of C . h
     float4 h[kK / 4][kStates][32 * kNW];
-    float sum[kNW][2][32];
+    // sums over all tokens, of chunks' sums in fp32: their terms cancel, and a thousand roundings of one fp32 sum would
+    // show in the result
+    double dA[kStates][32 * kNW], sum[kNW][2][32];
 };
 // Blocks an SM of the second pass: 384 threads with 168 registers each (the decays of a chunk are 64 of them),
 // where keeping the states there too left room for 256.
@@ -187,27 +293,27 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
     extern __shared__ __align__(16) unsigned char smem_raw[];
     BwdSmem<T, kNW, kK>& s = *reinterpret_cast<BwdSmem<T, kNW, kK>*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Where w = where(p.cblocks);
-    const int cblk = (int)(blockIdx.x % p.cblocks);
+    const Where w = where(p);
     const int c = w.c0 + lane;
     const bool on = c < p.C;
-    const int len = length_of(p.lengths, w.b, p.T);
+    const int len = w.len;
     const int n_chunks = (len + kK - 1) / kK;
     const int n0 = warp * kStates;
-    const long long row0 = (long long)w.b * p.T;
-    float a2[kStates], g[kStates], dA[kStates], first[kStates];
+    const long long row0 = (long long)w.b * p.T + w.t0;
+    float a2[kStates], g[kStates], first[kStates];
 #pragma unroll
     for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N;
         a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
         g[i] = live && p.dh_T ? p.dh_T[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
-        dA[i] = 0.f;
+        s.dA[i][tid] = 0.0;
     }
+    if (on) fold<kNp>(g, p, w.b, p.segs - 1, -1, p.segs - 1 - w.seg, 1, n0, c);
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f, skip = on && p.D ? p.D[c] : 0.f;
-    float dD = 0.f, dbias = 0.f;
+    double dD = 0.0, dbias = 0.0;
 
     // rows of padding: zero gradients
-    for (int t = len + warp; t < p.T; t += kNW) {
+    for (int t = len + warp; t < w.T; t += kNW) {
         if (on) {
             const size_t at = ((size_t)row0 + t) * p.C + c;
             const float zero[1] = {0.f};
@@ -230,7 +336,7 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const auto load_first = [&](int chunk) {
-        const float* in = p.ckpt + (((size_t)w.b * p.chunks + chunk) * kNp + n0) * p.C + c;
+        const float* in = p.ckpt + (((size_t)w.b * p.chunks + w.t0 / kK + chunk) * kNp + n0) * p.C + c;
 #pragma unroll
         for (int i = 0; i < kStates; i++) first[i] = on ? in[(size_t)i * p.C] : 0.f;
     };
@@ -306,6 +412,7 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
             }
         }
         if (chunk > 0) load_first(chunk - 1);
+        float dA[kStates] = {};
 #pragma unroll
         for (int q = kQ - 1; q >= 0; q--) {
             asm volatile("" ::: "memory");  // the loads of one quad at a time: hoisted together they spill
@@ -355,10 +462,13 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
             const float sum = sum_scatter(v, lane);
             const int t = chunk * kK + 4 * q + (lane >> 3), n = n0 + (lane & 3);
             if (t < len && n < p.N)
-                p.part_bc[((((size_t)cblk * p.B + w.b) * p.T + t) * 2 + ((lane >> 2) & 1)) * p.N + n] = sum;
+                p.part_bc[((((size_t)w.cblk * p.B + w.b) * p.T + w.t0 + t) * 2 + ((lane >> 2) & 1)) * p.N + n] = sum;
         }
+#pragma unroll
+        for (int i = 0; i < kStates; i++) s.dA[i][tid] += dA[i];
         __syncthreads();
         for (int q = warp; q < kQ; q += kNW) {
+            float sum_D = 0.f, sum_bias = 0.f;
             float4 gb = s.h[q][0][lane], ga = s.h[q][1][lane], y = s.h[q][2][lane];
 #pragma unroll
             for (int k = 1; k < kNW; k++) {
@@ -386,31 +496,34 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
                     const float o_z[1] = {dzs[k] * fmaf(skip, u, ys[k])};
                     store_vec<1>(static_cast<T*>(p.dz) + at, o_z);
                 }
-                dD = fmaf(dys[k], u, dD);
-                dbias += o_dt[0];
+                sum_D = fmaf(dys[k], u, sum_D);
+                sum_bias += o_dt[0];
             }
+            dD += sum_D;
+            dbias += sum_bias;
         }
     }
     s.sum[warp][0][lane] = dD;
     s.sum[warp][1][lane] = dbias;
     __syncthreads();
     if (on) {
+        const size_t row = (size_t)w.b * p.segs + w.seg;
 #pragma unroll
         for (int i = 0; i < kStates; i++) {
             if (n0 + i < p.N) {
-                p.part_c[((size_t)w.b * (p.N + 2) + n0 + i) * p.C + c] = dA[i];
-                if (p.dh0) p.dh0[((size_t)w.b * p.C + c) * p.N + n0 + i] = g[i];
+                p.part_c[(row * (p.N + 2) + n0 + i) * p.C + c] = (float)s.dA[i][tid];
+                if (p.dh0 && w.seg == 0) p.dh0[((size_t)w.b * p.C + c) * p.N + n0 + i] = g[i];
             }
         }
         if (warp == 0) {
-            float x = 0.f, y = 0.f;
+            double x = 0.0, y = 0.0;
 #pragma unroll
             for (int q = 0; q < kNW; q++) {
                 x += s.sum[q][0][lane];
                 y += s.sum[q][1][lane];
             }
-            p.part_c[((size_t)w.b * (p.N + 2) + p.N) * p.C + c] = x;
-            p.part_c[((size_t)w.b * (p.N + 2) + p.N + 1) * p.C + c] = y;
+            p.part_c[(row * (p.N + 2) + p.N) * p.C + c] = (float)x;
+            p.part_c[(row * (p.N + 2) + p.N + 1) * p.C + c] = (float)y;
         }
     }
 }
@@ -431,20 +544,29 @@ __global__ void __launch_bounds__(256) ttt_ssm_bc_sum_kernel(int B, int T, int N
     (m < N ? dB : dC)[((size_t)b * T + t) * N + (m < N ? m : m - N)] = a;
 }
 
-__global__ void __launch_bounds__(256) ttt_ssm_channel_sum_kernel(int B, int C, int N, const float* __restrict__ part,
+// 32 columns a block; its eight warps share out the rows
+__global__ void __launch_bounds__(256) ttt_ssm_channel_sum_kernel(int rows, int C, int N, const float* __restrict__ part,
                                                                   float* __restrict__ dA, float* __restrict__ dD,
                                                                   float* __restrict__ dbias) {
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (size_t)(N + 2) * C) return;
+    __shared__ double sums[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t cols = (size_t)(N + 2) * C, i = (size_t)blockIdx.x * 32 + lane;
+    double a = 0.0;
+    if (i < cols) {
+#pragma unroll 4
+        for (int r = warp; r < rows; r += 8) a += part[(size_t)r * cols + i];
+    }
+    sums[warp][lane] = a;
+    __syncthreads();
+    if (warp != 0 || i >= cols) return;
+    for (int k = 1; k < 8; k++) a += sums[k][lane];
     const int n = (int)(i / C), c = (int)(i % C);
-    float a = 0.f;
-    for (int b = 0; b < B; b++) a += part[(size_t)b * (N + 2) * C + i];
     if (n < N)
-        dA[(size_t)c * N + n] = a;
+        dA[(size_t)c * N + n] = (float)a;
     else if (n == N) {
-        if (dD) dD[c] = a;
+        if (dD) dD[c] = (float)a;
     } else if (dbias) {
-        dbias[c] = a;
+        dbias[c] = (float)a;
     }
 }
 
@@ -452,8 +574,26 @@ constexpr int warps_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 
 // 16 tokens a chunk keep 64 decays in registers; with 16 warps a thread has 128 registers in all, so 8 there
 constexpr int chunk_for(int kNW) { return kNW <= 8 ? 16 : 8; }
 
+// Parts of the time axis.  A launch of few blocks waits on its own results, some 600 clocks a token.  So where the blocks
+// fill at most half of the places that the SMs have for them, the axis is split into as many parts as there are
+// places for, whole tiles each and at most 64, which is what the walk over the parts' ends costs.  Measured, split
+// against whole (bf16, 16 states, 444 places): 4 blocks of 2641 tokens 60 us against 898, 36 of 614 77 against 320,
+// 128 of 1024 242 against 363, 192 of 1024 348 against 414.
+struct Split {
+    int segs, seg_len;
+};
+Split split_of(int B, int T, int C, int N) {
+    const int nw = warps_for(N), tile = 2 * chunk_for(nw);
+    const long long blocks = (long long)B * ((C + 31) / 32), places = 148LL * blocks_for(nw);
+    const int tiles = (int)(((long long)T + tile - 1) / tile);
+    if (2 * blocks > places || tiles < 2) return {1, tiles > 0 ? tiles * tile : tile};
+    const long long want = std::min<long long>({places / blocks, tiles, 64});
+    const int per = (int)((tiles + want - 1) / want);
+    return {(tiles + per - 1) / per, per * tile};
+}
+
 struct Layout {
-    size_t ckpt, part_bc, part_c, total;  // floats
+    size_t ckpt, part_bc, part_c, carry, total;  // floats
 };
 Layout layout(int B, int T, int C, int N) {
     const int nw = warps_for(N), K = chunk_for(nw);
@@ -462,21 +602,31 @@ Layout layout(int B, int T, int C, int N) {
     Layout l{};
     l.ckpt = up((size_t)B * chunks * kStates * nw * C);
     l.part_bc = up(cblocks * B * T * 2 * N);
-    l.part_c = up((size_t)B * (N + 2) * C);
-    l.total = l.ckpt + l.part_bc + l.part_c;
+    const size_t segs = (size_t)split_of(B, T, C, N).segs;
+    l.part_c = up(B * segs * (N + 2) * C);
+    l.carry = segs > 1 ? up(B * segs * 3 * kStates * nw * C) : 0;
+    l.total = l.ckpt + l.part_bc + l.part_c + l.carry;
     return l;
 }
 
 template <typename T, int kNW>
 cudaError_t launch(const SsmBwdParams& p, cudaStream_t stream) {
     constexpr int kK = chunk_for(kNW);
-    const unsigned grid = (unsigned)((long long)p.B * p.cblocks);
-    const auto first = ttt_ssm_checkpoint_kernel<T, kNW, kK>;
+    const unsigned grid = (unsigned)((long long)p.B * p.segs * p.cblocks);
+    const auto ends = ttt_ssm_checkpoint_kernel<T, kNW, kK, true>;
+    const auto first = ttt_ssm_checkpoint_kernel<T, kNW, kK, false>;
     const auto second = ttt_ssm_backward_kernel<T, kNW, kK>;
-    constexpr int smem1 = (int)sizeof(CkptSmem<T, kNW, 2 * kK>), smem2 = (int)sizeof(BwdSmem<T, kNW, kK>);
-    static_assert(smem1 <= (int)kMaxSmem && smem2 <= (int)kMaxSmem, "fits an SM");
+    constexpr int smem0 = (int)sizeof(CkptSmem<T, kNW, 2 * kK, true>), smem1 = (int)sizeof(CkptSmem<T, kNW, 2 * kK, false>);
+    constexpr int smem2 = (int)sizeof(BwdSmem<T, kNW, kK>);
+    static_assert(smem0 <= (int)kMaxSmem && smem1 <= (int)kMaxSmem && smem2 <= (int)kMaxSmem, "fits an SM");
     cudaError_t e = cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, smem1);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(second, cudaFuncAttributeMaxDynamicSharedMemorySize, smem2);
+    if (e == cudaSuccess && p.segs > 1) {
+        e = cudaFuncSetAttribute(ends, cudaFuncAttributeMaxDynamicSharedMemorySize, smem0);
+        if (e != cudaSuccess) return e;
+        ends<<<grid, 32 * kNW, smem0, stream>>>(p);
+        e = cudaPeekAtLastError();
+    }
     if (e != cudaSuccess) return e;
     first<<<grid, 32 * kNW, smem1, stream>>>(p);
     e = cudaPeekAtLastError();
@@ -514,7 +664,10 @@ cudaError_t launch_ssm_backward(const SsmBwdArgs& a, float* workspace, cudaStrea
     const int K = chunk_for(warps_for(f.N));
     p.chunks = (f.T + K - 1) / K;
     p.cblocks = (f.C + 31) / 32;
-    if ((long long)p.B * p.cblocks >= (1LL << 31)) return cudaErrorInvalidValue;
+    const Split split = split_of(f.B, f.T, f.C, f.N);
+    p.segs = split.segs;
+    p.seg_len = split.seg_len;
+    if ((long long)p.B * p.segs * p.cblocks >= (1LL << 31)) return cudaErrorInvalidValue;
     p.ld_u = f.ld_u;
     p.ld_dt = f.ld_dt;
     p.ld_b = f.ld_b;
@@ -540,6 +693,7 @@ cudaError_t launch_ssm_backward(const SsmBwdArgs& a, float* workspace, cudaStrea
     p.ckpt = workspace;
     p.part_bc = workspace + l.ckpt;
     p.part_c = p.part_bc + l.part_bc;
+    p.carry = p.part_c + l.part_c;
     const int es = f.dtype == TTT_BF16 ? 2 : 4;
     p.vec_rows = rows16(f.u, f.ld_u, f.C, es) && rows16(f.dt, f.ld_dt, f.C, es) && rows16(f.z, f.ld_z, f.C, es) &&
                  rows16(a.dy, f.C, f.C, es);
@@ -554,8 +708,8 @@ cudaError_t launch_ssm_backward(const SsmBwdArgs& a, float* workspace, cudaStrea
         if (e != cudaSuccess) return e;
     }
     const size_t ch = (size_t)(f.N + 2) * f.C;
-    ttt_ssm_channel_sum_kernel<<<(unsigned)((ch + 255) / 256), 256, 0, stream>>>(f.B, f.C, f.N, p.part_c, a.dA, a.dD,
-                                                                                 a.ddt_bias);
+    ttt_ssm_channel_sum_kernel<<<(unsigned)((ch + 31) / 32), 256, 0, stream>>>(f.B * p.segs, f.C, f.N, p.part_c, a.dA, a.dD,
+                                                                                a.ddt_bias);
     return cudaPeekAtLastError();
 }
 

@@ -99,6 +99,22 @@ def test_backward(ttt, B, T, d, past, kind):
     bc.close("dweight", dw, dwo, dwe)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,d", [(64, 300, 5), (8, 1000, 64), (3, 2000, 96), (1, 4000, 200)])
+def test_many_narrow_rows(ttt, B, T, d, kind):
+    """Several rows a block, and more rows than the blocks take at once."""
+    x, r, w = inputs(B, T, d, kind, True, seed=3)
+    y, h = ttt.ttt_rmsnorm_forward(x.cuda(), w.cuda(), r.cuda())
+    (yo, ye), (ho, he) = ob.rmsnorm(x, w, r)
+    bc.close("y", y, yo, ye)
+    bc.close("h", h, ho, he)
+    dy = bc.normal(torch.Generator().manual_seed(10), B, T, d).to(x.dtype)
+    dh, dw = ttt.ttt_rmsnorm_backward(x.cuda(), w.cuda(), dy.cuda(), r.cuda())
+    (dho, dhe), (dwo, dwe) = ob.rmsnorm_backward(x, w, dy, r)
+    bc.close("dh", dh, dho, dhe)
+    bc.close("dweight", dw, dwo, dwe)
+
+
 def test_backward_twice_is_the_same(ttt):
     x, r, w = (t.cuda() for t in inputs(4, 999, 512, "bf16", True))
     one, two = (ttt.ttt_rmsnorm_backward(x, w, r) for _ in range(2))

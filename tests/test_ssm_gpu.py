@@ -231,6 +231,38 @@ def test_backward_few_rows_long(ttt, B, T, C, N):
     check_backward(backward(ttt, bc.cuda(i), dy.cuda(), dh.cuda()), i, dy, dh)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("C,N", [(40, 16), (37, 3), (32, 30), (9, 64)])
+def test_backward_in_parts_of_a_padded_batch(ttt, C, N, kind):
+    """Few channels and hundreds of tokens: the time axis is split; sequences end in its first, a middle and its last part."""
+    B, T = 4, 333
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=18)
+    g = torch.Generator().manual_seed(19)
+    n = torch.tensor([T, 0, 5, 170], dtype=torch.int32)
+    dy, dh = bc.normal(g, B, T, C).to(i["u"].dtype), bc.normal(g, B, C, N)
+    for b in range(B):
+        dy[b, n[b]:] = NAN
+        for k in ("u", "dt", "Bm", "Cm", "z"):
+            i[k][b, n[b]:] = NAN
+    out = backward(ttt, bc.cuda(i), dy.cuda(), dh.cuda(), lengths=n.cuda())
+    check_backward(out, i, dy, dh, lengths=n)
+    for b in range(B):
+        for k in ("du", "ddt", "dz", "dB", "dC"):
+            assert not out[k][b, n[b]:].any(), k
+
+
+def test_backward_in_parts_of_growing_states(ttt):
+    i = bc.ssm_inputs(1, 200, 33, 8, "f32", seed=20, softplus=False)
+    i["A"] = -0.05 * i["A"]
+    dy = bc.normal(torch.Generator().manual_seed(21), 1, 200, 33)
+    check_backward(backward(ttt, bc.cuda(i), dy.cuda(), dt_softplus=False), i, dy, None, softplus=False)
+    # a decay that overflows over a part, and nothing for it to carry: zeros, no NaN
+    i = {k: torch.zeros_like(v) for k, v in bc.ssm_inputs(1, 8192, 8, 4, "f32", seed=22).items()}
+    i["A"], i["dt"] = i["A"] + 1.0, i["dt"] + 1.0
+    out = backward(ttt, bc.cuda(i), torch.zeros(1, 8192, 8, device="cuda"), dt_softplus=False)
+    assert all(not v.any() for v in out.values())
+
+
 def test_backward_twice_is_the_same(ttt):
     i = bc.cuda(bc.ssm_inputs(3, 300, 200, 16, "bf16", seed=17))
     one, two = backward(ttt, i, i["u"]), backward(ttt, i, i["u"])
