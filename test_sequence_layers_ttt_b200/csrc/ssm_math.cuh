@@ -68,6 +68,9 @@ __device__ __forceinline__ void decays(float (&a)[2 * kPairs], const f2 (&x)[kPa
     }
 }
 
+// a v + e; 0 becomes e where the decay over many tokens, of a growing state, has overflowed
+__device__ __forceinline__ float carried(float v, float a, float e) { return v == 0.f ? e : fmaf(a, v, e); }
+
 __device__ __forceinline__ int length_of(const int* lengths, int b, int T) {
     if (!lengths) return T;
     const int n = lengths[b];

@@ -69,8 +69,6 @@ template <int kNp>
 __device__ __forceinline__ size_t carry_at(const SsmBwdParams& p, int b, int seg, int m, int n0, int c) {
     return ((((size_t)b * p.segs + seg) * 3 + m) * kNp + n0) * p.C + c;
 }
-// a v + e; 0 becomes e where the decay of a whole part, of a growing state, has overflowed
-__device__ __forceinline__ float carried(float v, float a, float e) { return v == 0.f ? e : fmaf(a, v, e); }
 // v folded over `count` parts from part `from` on, in steps of `by`; m as in carry_at.  Eight parts' values are on
 // their way at a time: one by one, 64 parts took longer than a walk along one of them.
 template <int kNp>

@@ -7,13 +7,17 @@
 // first state, and runs its tokens again from there.  The special functions are evaluated once a token and
 // state all the same, and a channel keeps eight warps' worth of independent tokens in flight, which is what
 // a launch of few channels needs: a token takes 61 clocks for 8 channels of 16 states (bf16), where a
-// recursion that walks one token at a time takes 75 and more.
+// recursion that walks one token at a time takes 75 and more.  Where even so most SMs have no block, the blocks of
+// a cluster share out the tokens of one sequence the same way, through each other's shared memory (kSplit).
 #include "ssm_params.cuh"
+
+#include <cooperative_groups.h>
 
 namespace ttt {
 namespace {
 
 using namespace ssm;
+namespace cg = cooperative_groups;
 
 constexpr int kSeg = 16;      // tokens a warp takes of a tile
 constexpr int kMaxWarps = 8;  // 128 tokens a tile; a thread's 64 decays and 64 inputs take 250 registers
@@ -49,24 +53,30 @@ struct SegSmem {
     }
 };
 
-template <typename T, int kL>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(const Params p, const int cblocks, const int n_pad) {
+// kSplit: the blocks of a cluster take `per` tokens each of the same channels, twice: from zero (block 0: from
+// h0) for the state at the end of their part, which the blocks after them read, and again from the state folded so.
+template <typename T, int kL, bool kSplit>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(const Params p, const int cblocks, const int n_pad, const int per) {
     constexpr int kQ = 32 / kL;
     constexpr int kOwn = kSeg / kQ;  // tokens whose elementwise work a lane does
     extern __shared__ __align__(16) unsigned char smem_raw[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
-    const int b = (int)(blockIdx.x / cblocks), c0 = (int)(blockIdx.x % cblocks) * kL;
+    const int rank = kSplit ? (int)cg::this_cluster().block_rank() : 0, ranks = kSplit ? (int)cg::this_cluster().num_blocks() : 1;
+    const int block = (int)blockIdx.x / ranks, b = block / cblocks, c0 = block % cblocks * kL;
     const int ch = lane / kQ, part = lane % kQ, c = c0 + ch;
     const bool on = c < p.C;
-    const int len = length_of(p.lengths, b, p.T);
+    const int first_t = kSplit ? (int)min((long long)rank * per, (long long)p.T) : 0;
+    const int T_own = kSplit ? min(p.T - first_t, per) : p.T;
+    const int len = max(min(length_of(p.lengths, b, p.T) - first_t, T_own), 0);
+    const long long row0 = (long long)b * p.T + first_t;
     const int tile = kSeg * warps, groups = n_pad / (kStates * kQ), pitch = tile + 4, shift = 31 - __clz(n_pad);
     const SegSmem<T, kL> s(smem_raw, tile, n_pad);
-    const T* u_rows = static_cast<const T*>(p.u) + (long long)b * p.T * p.ld_u + c0;
-    const T* dt_rows = static_cast<const T*>(p.dt) + (long long)b * p.T * p.ld_dt + c0;
-    const T* z_rows = static_cast<const T*>(p.z) + (long long)b * p.T * p.ld_z + c0;
-    const T* b_rows = static_cast<const T*>(p.Bm) + (long long)b * p.T * p.ld_b;
-    const T* c_rows = static_cast<const T*>(p.Cm) + (long long)b * p.T * p.ld_c;
-    T* y_rows = static_cast<T*>(p.y) + (long long)b * p.T * p.C + c;
+    const T* u_rows = static_cast<const T*>(p.u) + row0 * p.ld_u + c0;
+    const T* dt_rows = static_cast<const T*>(p.dt) + row0 * p.ld_dt + c0;
+    const T* z_rows = static_cast<const T*>(p.z) + row0 * p.ld_z + c0;
+    const T* b_rows = static_cast<const T*>(p.Bm) + row0 * p.ld_b;
+    const T* c_rows = static_cast<const T*>(p.Cm) + row0 * p.ld_c;
+    T* y_rows = static_cast<T*>(p.y) + row0 * p.C + c;
 
     const auto stage = [&](int t0, int buf) {
         const int width = p.C - c0;
@@ -83,7 +93,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
 #pragma unroll
         for (int i = 0; i < kStates; i++) {
             const int n = (g * kQ + part) * kStates + i;
-            h[i] = on && n < p.N && p.h0 ? p.h0[((size_t)b * p.C + c) * p.N + n] : 0.f;
+            h[i] = on && n < p.N && p.h0 && rank == 0 ? p.h0[((size_t)b * p.C + c) * p.N + n] : 0.f;
             v[i] = on && n < p.N ? p.A[(size_t)c * p.N + n] * kLog2e : 0.f;
         }
         s.h[g * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
@@ -91,154 +101,201 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
     }
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f, skip = on && p.D ? p.D[c] : 0.f;
 
-    if (len > 0) stage(0, 0);
     int turn = 0, buf = 0;  // turn: which of the two segment buffers
-    for (int t0 = 0; t0 < len; t0 += tile, buf ^= 1) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncthreads();
-        if (t0 + tile < len) stage(t0 + tile, buf ^ 1);
-        for (int i = tid; i < tile * n_pad; i += threads) {
-            const int at = (i & (n_pad - 1)) * pitch + (i >> shift);
-            s.b[at] = to_f32(s.rb[buf * tile * n_pad + i]);
-            s.c[at] = to_f32(s.rc[buf * tile * n_pad + i]);
-        }
-        const int k0 = warp * kSeg;
-        f2 dt2[kSeg / 2], du2[kSeg / 2], y2[kSeg / 2];  // of the warp's tokens, in pairs
-        float own_u[kOwn], sum_dt = 0.f;
-        {
-            float own_dt[kOwn];
-#pragma unroll
-            for (int j = 0; j < kOwn; j++) {
-                const int k = k0 + part * kOwn + j;
-                float d = to_f32(s.dt[(buf * tile + k) * kL + ch]) + bias;
-                if (p.softplus) d = ssm::softplus(d);
-                own_dt[j] = t0 + k < len ? d : 0.f;
-                own_u[j] = to_f32(s.u[(buf * tile + k) * kL + ch]);
+    float all_dt = 0.f;     // of the warp's tokens of all tiles
+#pragma unroll 1
+    for (int pass = kSplit ? 0 : 1; pass < 2; pass++) {
+        const bool ends = kSplit && pass == 0;
+        if (len > 0) stage(0, buf);
+        for (int t0 = 0; t0 < len; t0 += tile, buf ^= 1) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
+            if (t0 + tile < len) stage(t0 + tile, buf ^ 1);
+            for (int i = tid; i < tile * n_pad; i += threads) {
+                const int at = (i & (n_pad - 1)) * pitch + (i >> shift);
+                s.b[at] = to_f32(s.rb[buf * tile * n_pad + i]);
+                s.c[at] = to_f32(s.rc[buf * tile * n_pad + i]);
             }
-            float dt[kSeg], du[kSeg];
+            const int k0 = warp * kSeg;
+            f2 dt2[kSeg / 2], du2[kSeg / 2], y2[kSeg / 2];  // of the warp's tokens, in pairs
+            float own_u[kOwn], sum_dt = 0.f;
+            {
+                float own_dt[kOwn];
 #pragma unroll
-            for (int k = 0; k < kSeg; k++) {
-                if constexpr (kQ == 1) {
-                    dt[k] = own_dt[k];
-                    du[k] = own_dt[k] * own_u[k];
-                } else {
-                    const int from = (lane & ~(kQ - 1)) + k / kOwn;
-                    dt[k] = __shfl_sync(0xffffffffu, own_dt[k % kOwn], from);
-                    du[k] = __shfl_sync(0xffffffffu, own_dt[k % kOwn] * own_u[k % kOwn], from);
+                for (int j = 0; j < kOwn; j++) {
+                    const int k = k0 + part * kOwn + j;
+                    float d = to_f32(s.dt[(buf * tile + k) * kL + ch]) + bias;
+                    if (p.softplus) d = ssm::softplus(d);
+                    own_dt[j] = t0 + k < len ? d : 0.f;
+                    own_u[j] = to_f32(s.u[(buf * tile + k) * kL + ch]);
                 }
-                sum_dt += dt[k];
-            }
+                float dt[kSeg], du[kSeg];
 #pragma unroll
-            for (int k = 0; k < kSeg / 2; k++) {
-                dt2[k] = pack2(dt[2 * k], dt[2 * k + 1]);
-                du2[k] = pack2(du[2 * k], du[2 * k + 1]);
-                y2[k] = pack2(0.f, 0.f);
-            }
-        }
-        __syncthreads();
-        for (int g = 0; g < groups; g++, turn ^= 1) {
-            const int n0 = (g * kQ + part) * kStates;
-            const float4 A4 = s.a2[g * 32 + lane];
-            const float a2[kStates] = {A4.x, A4.y, A4.z, A4.w};
-            float a[kStates][kSeg], h[kStates];
-            f2 in[kStates][kSeg / 2];
-#pragma unroll
-            for (int i = 0; i < kStates; i++) {
-                const f2 A2 = pack2(a2[i], a2[i]);
-                f2 x[kSeg / 2];
-#pragma unroll
-                for (int k = 0; k < kSeg / 2; k++) x[k] = mul2(dt2[k], A2);
-                decays<kSeg / 2>(a[i], x);
-                const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[(n0 + i) * pitch + k0]);
-#pragma unroll
-                for (int k = 0; k < kSeg / 4; k++) {
-                    const ulonglong2 Bk = Bi[k];
-                    in[i][2 * k] = mul2(du2[2 * k], Bk.x);
-                    in[i][2 * k + 1] = mul2(du2[2 * k + 1], Bk.y);
+                for (int k = 0; k < kSeg; k++) {
+                    if constexpr (kQ == 1) {
+                        dt[k] = own_dt[k];
+                        du[k] = own_dt[k] * own_u[k];
+                    } else {
+                        const int from = (lane & ~(kQ - 1)) + k / kOwn;
+                        dt[k] = __shfl_sync(0xffffffffu, own_dt[k % kOwn], from);
+                        du[k] = __shfl_sync(0xffffffffu, own_dt[k % kOwn] * own_u[k % kOwn], from);
+                    }
+                    sum_dt += dt[k];
                 }
-                h[i] = 0.f;
+                all_dt += sum_dt;
 #pragma unroll
                 for (int k = 0; k < kSeg / 2; k++) {
-                    float lo, hi;
-                    unpack2(in[i][k], lo, hi);
-                    h[i] = fmaf(a[i][2 * k], h[i], lo);
-                    h[i] = fmaf(a[i][2 * k + 1], h[i], hi);
+                    dt2[k] = pack2(dt[2 * k], dt[2 * k + 1]);
+                    du2[k] = pack2(du[2 * k], du[2 * k + 1]);
+                    y2[k] = pack2(0.f, 0.f);
                 }
             }
-            s.end[(turn * kMaxWarps + warp) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
-            s.fall[(turn * kMaxWarps + warp) * 32 + lane] =
-                make_float4(decay(sum_dt * a2[0]), decay(sum_dt * a2[1]), decay(sum_dt * a2[2]), decay(sum_dt * a2[3]));
             __syncthreads();
-            const float4 first = s.h[(buf * groups + g) * 32 + lane];
-            h[0] = first.x;
-            h[1] = first.y;
-            h[2] = first.z;
-            h[3] = first.w;
-            for (int v = 0; v < warp; v++) {
-                const float4 e = s.end[(turn * kMaxWarps + v) * 32 + lane], f = s.fall[(turn * kMaxWarps + v) * 32 + lane];
-                h[0] = fmaf(f.x, h[0], e.x);
-                h[1] = fmaf(f.y, h[1], e.y);
-                h[2] = fmaf(f.z, h[2], e.z);
-                h[3] = fmaf(f.w, h[3], e.w);
-            }
-#pragma unroll
-            for (int k = 0; k < kSeg / 4; k++) {
-                float hk[kStates][4];
+            for (int g = 0; g < groups; g++, turn ^= 1) {
+                const int n0 = (g * kQ + part) * kStates;
+                const float4 A4 = s.a2[g * 32 + lane];
+                const float a2[kStates] = {A4.x, A4.y, A4.z, A4.w};
+                float a[kStates][kSeg], h[kStates];
+                f2 in[kStates][kSeg / 2];
 #pragma unroll
                 for (int i = 0; i < kStates; i++) {
+                    const f2 A2 = pack2(a2[i], a2[i]);
+                    f2 x[kSeg / 2];
 #pragma unroll
-                    for (int q = 0; q < 2; q++) {
+                    for (int k = 0; k < kSeg / 2; k++) x[k] = mul2(dt2[k], A2);
+                    decays<kSeg / 2>(a[i], x);
+                    const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[(n0 + i) * pitch + k0]);
+#pragma unroll
+                    for (int k = 0; k < kSeg / 4; k++) {
+                        const ulonglong2 Bk = Bi[k];
+                        in[i][2 * k] = mul2(du2[2 * k], Bk.x);
+                        in[i][2 * k + 1] = mul2(du2[2 * k + 1], Bk.y);
+                    }
+                    h[i] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kSeg / 2; k++) {
                         float lo, hi;
-                        unpack2(in[i][2 * k + q], lo, hi);
-                        hk[i][2 * q] = h[i] = fmaf(a[i][4 * k + 2 * q], h[i], lo);
-                        hk[i][2 * q + 1] = h[i] = fmaf(a[i][4 * k + 2 * q + 1], h[i], hi);
+                        unpack2(in[i][k], lo, hi);
+                        h[i] = fmaf(a[i][2 * k], h[i], lo);
+                        h[i] = fmaf(a[i][2 * k + 1], h[i], hi);
                     }
                 }
+                s.end[(turn * kMaxWarps + warp) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+                s.fall[(turn * kMaxWarps + warp) * 32 + lane] =
+                    make_float4(decay(sum_dt * a2[0]), decay(sum_dt * a2[1]), decay(sum_dt * a2[2]), decay(sum_dt * a2[3]));
+                __syncthreads();
+                const float4 first = s.h[(buf * groups + g) * 32 + lane];
+                h[0] = first.x;
+                h[1] = first.y;
+                h[2] = first.z;
+                h[3] = first.w;
+                for (int v = 0; v < warp + (ends ? 1 : 0); v++) {
+                    const float4 e = s.end[(turn * kMaxWarps + v) * 32 + lane], f = s.fall[(turn * kMaxWarps + v) * 32 + lane];
+                    h[0] = fmaf(f.x, h[0], e.x);
+                    h[1] = fmaf(f.y, h[1], e.y);
+                    h[2] = fmaf(f.z, h[2], e.z);
+                    h[3] = fmaf(f.w, h[3], e.w);
+                }
+                if (ends) {
+                    if (warp == warps - 1) s.h[((buf ^ 1) * groups + g) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+                    continue;
+                }
 #pragma unroll
-                for (int i = 0; i < kStates; i++) {
-                    const ulonglong2 Ck = *reinterpret_cast<const ulonglong2*>(&s.c[(n0 + i) * pitch + k0 + 4 * k]);
-                    y2[2 * k] = fma2(Ck.x, pack2(hk[i][0], hk[i][1]), y2[2 * k]);
-                    y2[2 * k + 1] = fma2(Ck.y, pack2(hk[i][2], hk[i][3]), y2[2 * k + 1]);
+                for (int k = 0; k < kSeg / 4; k++) {
+                    float hk[kStates][4];
+#pragma unroll
+                    for (int i = 0; i < kStates; i++) {
+#pragma unroll
+                        for (int q = 0; q < 2; q++) {
+                            float lo, hi;
+                            unpack2(in[i][2 * k + q], lo, hi);
+                            hk[i][2 * q] = h[i] = fmaf(a[i][4 * k + 2 * q], h[i], lo);
+                            hk[i][2 * q + 1] = h[i] = fmaf(a[i][4 * k + 2 * q + 1], h[i], hi);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kStates; i++) {
+                        const ulonglong2 Ck = *reinterpret_cast<const ulonglong2*>(&s.c[(n0 + i) * pitch + k0 + 4 * k]);
+                        y2[2 * k] = fma2(Ck.x, pack2(hk[i][0], hk[i][1]), y2[2 * k]);
+                        y2[2 * k + 1] = fma2(Ck.y, pack2(hk[i][2], hk[i][3]), y2[2 * k + 1]);
+                    }
+                }
+                if (warp == warps - 1) s.h[((buf ^ 1) * groups + g) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+            }
+            if (ends) continue;
+            float y[kSeg];
+#pragma unroll
+            for (int k = 0; k < kSeg / 2; k++) unpack2(y2[k], y[2 * k], y[2 * k + 1]);
+            // a channel's lanes share out the tokens: kOwn sums each
+            float own_y[kOwn];
+            if constexpr (kQ == 1) {
+#pragma unroll
+                for (int j = 0; j < kOwn; j++) own_y[j] = y[j];
+            } else {
+                static_assert(kQ == 1 || kQ == 4, "two exchange steps");
+                const bool up2 = part & 2, up1 = part & 1;
+                float half[kSeg / 2];
+#pragma unroll
+                for (int j = 0; j < kSeg / 2; j++) {
+                    const float keep = up2 ? y[kSeg / 2 + j] : y[j], send = up2 ? y[j] : y[kSeg / 2 + j];
+                    half[j] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
+                }
+#pragma unroll
+                for (int j = 0; j < kSeg / 4; j++) {
+                    const float keep = up1 ? half[kSeg / 4 + j] : half[j], send = up1 ? half[j] : half[kSeg / 4 + j];
+                    own_y[j] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
                 }
             }
-            if (warp == warps - 1) s.h[((buf ^ 1) * groups + g) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
-        }
-        float y[kSeg];
 #pragma unroll
-        for (int k = 0; k < kSeg / 2; k++) unpack2(y2[k], y[2 * k], y[2 * k + 1]);
-        // a channel's lanes share out the tokens: kOwn sums each
-        float own_y[kOwn];
-        if constexpr (kQ == 1) {
-#pragma unroll
-            for (int j = 0; j < kOwn; j++) own_y[j] = y[j];
-        } else {
-            static_assert(kQ == 1 || kQ == 4, "two exchange steps");
-            const bool up2 = part & 2, up1 = part & 1;
-            float half[kSeg / 2];
-#pragma unroll
-            for (int j = 0; j < kSeg / 2; j++) {
-                const float keep = up2 ? y[kSeg / 2 + j] : y[j], send = up2 ? y[j] : y[kSeg / 2 + j];
-                half[j] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
-            }
-#pragma unroll
-            for (int j = 0; j < kSeg / 4; j++) {
-                const float keep = up1 ? half[kSeg / 4 + j] : half[j], send = up1 ? half[j] : half[kSeg / 4 + j];
-                own_y[j] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+            for (int j = 0; j < kOwn; j++) {
+                const int k = k0 + part * kOwn + j, t = t0 + k;
+                float o[1] = {fmaf(skip, own_u[j], own_y[j])};
+                if (p.z) {
+                    const float z = to_f32(s.z[(buf * tile + k) * kL + ch]);
+                    o[0] *= z * sigmoid(z);
+                }
+                if (on && t < len) store_vec<1>(y_rows + (long long)t * p.C, o);
             }
         }
-#pragma unroll
-        for (int j = 0; j < kOwn; j++) {
-            const int k = k0 + part * kOwn + j, t = t0 + k;
-            float o[1] = {fmaf(skip, own_u[j], own_y[j])};
-            if (p.z) {
-                const float z = to_f32(s.z[(buf * tile + k) * kL + ch]);
-                o[0] *= z * sigmoid(z);
+        __syncthreads();
+        if constexpr (kSplit) {
+            if (!ends) continue;
+            // the segments' buffers are free: the part's end states go to `end`, its decays to `fall`
+            float* sums = reinterpret_cast<float*>(s.end);
+            sums[warp * 32 + lane] = all_dt;
+            __syncthreads();
+            float total = 0.f;
+            for (int v = 0; v < warps; v++) total += sums[v * 32 + lane];
+            __syncthreads();
+            for (int g = warp; g < groups; g += warps) {
+                const float4 A4 = s.a2[g * 32 + lane];
+                s.end[g * 32 + lane] = s.h[(buf * groups + g) * 32 + lane];
+                s.fall[g * 32 + lane] = make_float4(decay(total * A4.x), decay(total * A4.y), decay(total * A4.z), decay(total * A4.w));
             }
-            if (on && t < len) store_vec<1>(y_rows + (long long)t * p.C, o);
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            for (int g = warp; g < groups && rank > 0; g += warps) {
+                float4 h = cluster.map_shared_rank(s.end, 0)[g * 32 + lane];
+                for (int r = 1; r < rank; r++) {
+                    const float4 e = cluster.map_shared_rank(s.end, r)[g * 32 + lane], f = cluster.map_shared_rank(s.fall, r)[g * 32 + lane];
+                    h = make_float4(carried(h.x, f.x, e.x), carried(h.y, f.y, e.y), carried(h.z, f.z, e.z), carried(h.w, f.w, e.w));
+                }
+                s.h[(buf * groups + g) * 32 + lane] = h;
+            }
+            if (rank == 0)
+                for (int g = warp; g < groups; g += warps) {
+                    float h[kStates];
+#pragma unroll
+                    for (int i = 0; i < kStates; i++) {
+                        const int n = (g * kQ + part) * kStates + i;
+                        h[i] = on && n < p.N && p.h0 ? p.h0[((size_t)b * p.C + c) * p.N + n] : 0.f;
+                    }
+                    s.h[(buf * groups + g) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+                }
+            cluster.sync();  // the others have read this block's ends; and h0, which h_T may replace, has been read
         }
     }
-    __syncthreads();
-    for (int g = warp; g < groups; g += warps) {
+    for (int g = warp; g < groups && rank == ranks - 1; g += warps) {  // the last block has the final state
         const float4 v = s.h[(buf * groups + g) * 32 + lane];
         const float h[kStates] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -248,8 +305,26 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
         }
     }
     const float zero[1] = {0.f};
-    for (int t = len + warp * kQ + part; t < p.T; t += warps * kQ)
+    for (int t = len + warp * kQ + part; t < T_own; t += warps * kQ)
         if (on) store_vec<1>(y_rows + (long long)t * p.C, zero);
+}
+
+template <typename T, int kL, bool kSplit>
+cudaError_t start(const Params& p, int cblocks, int n_pad, int per, int ranks, int warps, size_t smem, cudaStream_t stream) {
+    const auto kernel = ttt_ssm_segments_kernel<T, kL, kSplit>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((long long)p.B * cblocks * ranks));
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)ranks, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = kSplit ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, cblocks, n_pad, per);
 }
 
 template <typename T, int kL>
@@ -265,11 +340,14 @@ cudaError_t launch(const SsmArgs& a, cudaStream_t stream) {
     int warps = segs < 1 ? 1 : (segs < kMaxWarps ? segs : kMaxWarps);
     while (warps > 1 && SegSmem<T, kL>::bytes(kSeg * warps, n_pad) > kMaxSmem) warps--;
     const size_t smem = SegSmem<T, kL>::bytes(kSeg * warps, n_pad);
-    const auto kernel = ttt_ssm_segments_kernel<T, kL>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)grid, 32 * warps, smem, stream>>>(p, (int)cblocks, n_pad);
-    return cudaPeekAtLastError();
+    const int tiles = (int)(((long long)a.T + kSeg * warps - 1) / (kSeg * warps));
+    int ranks = 1;
+    // Blocks of a cluster share out the tokens as long as all clusters run at once: 15 of eight blocks, 32 of four
+    // (16 of eight, measured, take two turns).  A split walk reads its inputs twice, so two blocks gain a tenth (4096 tokens,
+    // 512 channels, 16 states: 117 us against 131), four half (256: 63 against 131), eight three quarters (64: 35 against 131).
+    while (ranks < 8 && 2 * ranks <= tiles && 2 * ranks * grid <= (ranks == 1 ? 148 : ranks == 2 ? 128 : 120)) ranks *= 2;
+    if (ranks == 1) return start<T, kL, false>(p, (int)cblocks, n_pad, 0, 1, warps, smem, stream);
+    return start<T, kL, true>(p, (int)cblocks, n_pad, (tiles + ranks - 1) / ranks * kSeg * warps, ranks, warps, smem, stream);
 }
 
 }  // namespace

@@ -178,6 +178,32 @@ def test_few_rows_long_padded(ttt):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,C,N", [(1, 3, 16), (3, 40, 16), (2, 100, 5), (3, 33, 40)])
+def test_few_rows_in_parts_with_the_state_in_place(ttt, B, C, N, kind):
+    """Several parts of the tokens, ragged ones, in a cluster; h_T takes h0's place."""
+    T = 1100
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=23)
+    n = torch.tensor([T, 130, 1000][:B], dtype=torch.int32)
+    c = bc.cuda(i)
+    y, h = forward(ttt, c, h_T=c["h0"], lengths=n.cuda())
+    assert h is c["h0"]
+    check_forward((y, h), i, lengths=n)
+    again = forward(ttt, bc.cuda(i), lengths=n.cuda())
+    assert torch.equal(y, again[0]) and torch.equal(h, again[1])
+
+
+def test_few_rows_in_parts_of_growing_states(ttt):
+    i = bc.ssm_inputs(1, 600, 20, 8, "f32", seed=24, softplus=False)
+    i["A"] = -0.02 * i["A"]
+    check_forward(forward(ttt, bc.cuda(i), dt_softplus=False), i, softplus=False)
+    # a decay that overflows over a part, and nothing for it to carry: zeros, no NaN
+    i = {k: torch.zeros_like(v) for k, v in bc.ssm_inputs(1, 8192, 8, 4, "f32", seed=25).items()}
+    i["A"], i["dt"] = i["A"] + 1.0, i["dt"] + 1.0
+    y, h = forward(ttt, bc.cuda(i), dt_softplus=False)
+    assert not y.any() and not h.any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,C,N", SIZES)
 def test_backward(ttt, B, T, C, N, kind):
     i = bc.ssm_inputs(B, T, C, N, kind, seed=100 + T)
