@@ -10,10 +10,15 @@
 //              reads zeros
 //   warp 1     TMEM allocation and the tcgen05 MMAs (kind f8f6f4, M = 128, N = 256, K = 32), fp32
 //              accumulators in two TMEM buffers of 256 columns
-//   warps 4-7  the epilogue (warp 4 + i reads TMEM lanes 32 i..32 i + 31, one token row per thread)
+//   warps 4-11 the epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31, one token row a thread, and two of the
+//              tile's four heads; a head's rows go out by TMA from a swizzled stage in shared memory
 // While the epilogue drains one accumulator the MMA warp fills the other.  Every wait is bounded: after
 // about a second without progress the kernel records an error word and stops waiting (outputs undefined;
 // TTT_ERR_TIMEOUT with TTT_CHECK=1).
+//
+// Measured (2 x 32768 tokens, d_model 2048, 32 heads): 0.70 ms, 2.4 PFLOP/s; without the epilogue's work 0.52 ms, with
+// all of it but the stores 0.58 ms.  The tensor pipe is busy for 67 % of the clocks.  Eight epilogue warps instead
+// of four, TMA stores and angles in fixed point took it there from 1.04 ms; a tile of 256 tokens in one CTA gave nothing.
 #include <cstdlib>
 
 #include "block_internal.h"

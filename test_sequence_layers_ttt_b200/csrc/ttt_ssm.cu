@@ -5,7 +5,8 @@
 // per channel, with N states a channel; B_t and C_t are shared by all channels of a token.
 //
 // For a token the state is nearly all there is to move (8 N bytes a channel, read and written), and for a
-// few streams the launch is all there is to wait for.
+// few streams the launch is all there is to wait for.  Measured: one token of 64 streams of 2048 channels, 16 states
+// (17 MB of state), 10 to 12 us replayed from a graph, 24 us a call with the host's share.
 #include "ssm_params.cuh"
 
 namespace ttt {
