@@ -267,7 +267,7 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                 // half step of 2^-8.  (In double the reduction took as long as both functions.)
                 f2 cs[16], sn[16];  // of two neighbouring features each
                 if (rope) {
-                    const unsigned long long pos = (unsigned long long)(long long)(p.pos0 + t);
+                    const unsigned long long pos = (unsigned long long)((long long)p.pos0 + t);
 #pragma unroll
                     for (int i = 0; i < 16; i++) {
                         float c[2], n[2];

@@ -56,6 +56,7 @@ def compare(out, ref, where=""):
     (2, 100, 4, 144, 0, True),      # rows and d_model end inside a tile
     (1, 300, 8, 256, 37, False),
     (3, 77, 12, 768, 100000, True),  # the 125M-layer width, ragged streams, far positions
+    (1, 40, 4, 64, 2 ** 31 - 20, True),  # positions that pass 31 bits: angles 2^-23 of a turn apart at most
     (1, 130, 20, 1040, 5, True),    # 20 heads: the learning-rate tile is padded to 32 columns
 ])
 def test_against_the_oracle(ttt, B, T, H, dm, pos0, rotary):
