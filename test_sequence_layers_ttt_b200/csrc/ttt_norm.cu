@@ -10,8 +10,8 @@
 // belongs to one group of threads (a part of a warp, a warp, or a block of up to 512), each holding kNV vectors of 16 bytes,
 // 16 elements where the row is long enough: with 8 the reduction, some 70 instructions a thread and row, took
 // as many as the elements.  A group walks rows with a stride and keeps its part of the weight; in the forward
-// the next row is on its way while one is worked on, in the backward, whose registers are full, other blocks of
-// the SM have theirs.  The sum of squares and the largest |h w| (y / scale is h w 448 / max |h w|,
+// the next row is on its way while one is worked on, and so it is in the backward of 16-bit rows; that of fp32 rows,
+// whose registers are full, has other blocks of the SM.  The sum of squares and the largest |h w| (y / scale is h w 448 / max |h w|,
 // without r) meet in one reduction, so 8 bits cost no second one.  Sums are in fp32; y, h, dh are rounded once.
 //
 // Measured: 2 x 32768 rows of 2048, bf16 with a residual and an 8-bit output, 165 us, 5.7 TB/s, 0.87 of the copy
@@ -243,25 +243,38 @@ __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwd
 #pragma unroll
         for (int k = 0; k < P; k++) dw[i][k] = pack2(0.f, 0.f);
     }
-    int buf = 0;
-    for (long long row = group; row - threadIdx.y < p.rows; row += groups, buf ^= 1) {
-        const int d = row < p.rows ? p.d : -V;
-        f2 h[kNV][P], dy[kNV][P], sq = pack2(0.f, 0.f), dot = sq;
-        Raw<T, V> rh[kNV], rg[kNV], past[kNV];
+    // 16-bit rows of up to 8192 leave registers for the next row of h and dy to be on its way (32768 rows of 2048: 95 us against 115)
+    constexpr bool kAhead = sizeof(T) == 2 && kNV <= 2;
+    Raw<T, V> rh[kNV], rg[kNV], past[kNV];
+    const auto fetch = [&](int d) {
 #pragma unroll
         for (int i = 0; i < kNV; i++) {
             const int at = place<V>(i, off);
             load_at<kShift>(rh[i], hp, at, d);
             load_at<kShift>(rg[i], gp, at, d);
-            if (ip) load_at<kShift>(past[i], ip, at, d);
         }
         hp += stride;
         gp += stride;
-        if (ip) ip += stride;
+    };
+    if (kAhead) fetch(group < p.rows ? p.d : -V);
+    int buf = 0;
+    for (long long row = group; row - threadIdx.y < p.rows; row += groups, buf ^= 1) {
+        const int d = row < p.rows ? p.d : -V;
+        f2 h[kNV][P], dy[kNV][P], sq = pack2(0.f, 0.f), dot = sq;
+        if (!kAhead) fetch(d);
+        if (ip) {
+#pragma unroll
+            for (int i = 0; i < kNV; i++) load_at<kShift>(past[i], ip, place<V>(i, off), d);
+            ip += stride;
+        }
 #pragma unroll
         for (int i = 0; i < kNV; i++) {
             pairs_of(rh[i], h[i]);
             pairs_of(rg[i], dy[i]);
+        }
+        if (kAhead) fetch(row + groups < p.rows ? p.d : -V);
+#pragma unroll
+        for (int i = 0; i < kNV; i++) {
 #pragma unroll
             for (int k = 0; k < P; k++) {
                 sq = fma2(h[i][k], h[i][k], sq);
