@@ -15,8 +15,9 @@
 // without r) meet in one reduction, so 8 bits cost no second one.  Sums are in fp32; y, h, dh are rounded once.
 //
 // Measured: 2 x 32768 rows of 2048, bf16 with a residual and an 8-bit output, 165 us, 5.7 TB/s, 0.87 of the copy
-// bandwidth; gradient of 3 x 2731 rows of 2047 in fp32, rows that start inside a
-// vector, 68 us, 4.0 TB/s: three blocks an SM, all that its registers hold, leave the memory waiting in the reductions.
+// bandwidth; gradient of 32768 rows of 2048 in bf16 95 us, 0.86 of it; of 3 x 2731 rows of 2047 in fp32, rows that start
+// inside a vector, 68 us, 4.0 TB/s: three blocks an SM, all that its registers hold, leave the memory waiting in the
+// reductions.  4096 rows of 9001 in fp32 97 us forward (0.92) and 164 backward (0.55, one block an SM).
 //
 // Where d is no multiple of a vector (kShift), rows start inside one: a group counts its vectors from the
 // 16-byte boundary before its row, and the two at the ends go element by element.  The stride is a multiple of
@@ -98,7 +99,7 @@ struct NormParams {
 };
 
 template <typename T, int kNV, bool kShift, bool kQ8>
-__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1) ttt_rmsnorm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(512, sizeof(T) == 2 && kNV <= 2 ? 2 : 1) ttt_rmsnorm_kernel(const NormParams p) {
     constexpr int V = Elem<T>::kVec, P = V / 2;
     __shared__ float2 s[2][16];
     const long long group = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -232,19 +233,34 @@ __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwd
     const T* gp = static_cast<const T*>(p.dy) + (size_t)group * p.d;
     const T* ip = p.dh_in ? static_cast<const T*>(p.dh_in) + (size_t)group * p.d : nullptr;
     const size_t stride = (size_t)groups * p.d;
-    f2 w[kNV][P], dw[kNV][P];
+    // Rows past 8192 leave no registers for the weight, which waits in shared memory (a thread's own part, 16 bytes
+    // side by side with its neighbours'), nor for h and dy in fp32 beside their 16 bits.
+    constexpr bool kWide = kNV * V > 16;
+    extern __shared__ ulonglong2 wide[];
+    const auto w_place = [&](int i, int k) -> ulonglong2& { return wide[(i * P / 2 + k) * blockDim.x + threadIdx.x]; };
+    f2 w[kWide ? 1 : kNV][P], dw[kNV][P];
 #pragma unroll
     for (int i = 0; i < kNV; i++) {
         const int at = place<V>(i, off);
         float v[V];
+        f2 wi[P];
 #pragma unroll
         for (int k = 0; k < V; k++) v[k] = at + k >= 0 && at + k < p.d ? p.weight[at + k] : 0.f;
-        to_pairs<V>(v, w[i]);
+        to_pairs<V>(v, wi);
+#pragma unroll
+        for (int k = 0; k < P / 2; k++) {
+            if (kWide) {
+                w_place(i, k) = make_ulonglong2(wi[2 * k], wi[2 * k + 1]);
+            } else {
+                w[kWide ? 0 : i][2 * k] = wi[2 * k];
+                w[kWide ? 0 : i][2 * k + 1] = wi[2 * k + 1];
+            }
+        }
 #pragma unroll
         for (int k = 0; k < P; k++) dw[i][k] = pack2(0.f, 0.f);
     }
     // 16-bit rows of up to 8192 leave registers for the next row of h and dy to be on its way (32768 rows of 2048: 95 us against 115)
-    constexpr bool kAhead = sizeof(T) == 2 && kNV <= 2;
+    constexpr bool kAhead = sizeof(T) == 2 && !kWide, kPastLate = sizeof(T) == 4 && kWide;
     Raw<T, V> rh[kNV], rg[kNV], past[kNV];
     const auto fetch = [&](int d) {
 #pragma unroll
@@ -260,25 +276,53 @@ __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwd
     int buf = 0;
     for (long long row = group; row - threadIdx.y < p.rows; row += groups, buf ^= 1) {
         const int d = row < p.rows ? p.d : -V;
-        f2 h[kNV][P], dy[kNV][P], sq = pack2(0.f, 0.f), dot = sq;
+        f2 kept_h[kWide ? 1 : kNV][P], kept_dy[kWide ? 1 : kNV][P], sq = pack2(0.f, 0.f), dot = sq;
         if (!kAhead) fetch(d);
-        if (ip) {
+        const auto fetch_past = [&] {
+            if (!ip) return;
 #pragma unroll
             for (int i = 0; i < kNV; i++) load_at<kShift>(past[i], ip, place<V>(i, off), d);
             ip += stride;
+        };
+        if (!kPastLate) fetch_past();
+        if constexpr (!kWide) {
+#pragma unroll
+            for (int i = 0; i < kNV; i++) {
+                pairs_of(rh[i], kept_h[i]);
+                pairs_of(rg[i], kept_dy[i]);
+            }
+            if (kAhead) fetch(row + groups < p.rows ? p.d : -V);
         }
+        // the i-th vector of h, dy and the weight
+        const auto values = [&](int i, f2(&h)[P], f2(&dy)[P], f2(&wi)[P]) {
+            if constexpr (kWide) {
+                pairs_of(rh[i], h);
+                pairs_of(rg[i], dy);
+            }
+#pragma unroll
+            for (int k = 0; k < P / 2; k++) {
+                if constexpr (kWide) {
+                    const ulonglong2 a = w_place(i, k);
+                    wi[2 * k] = a.x;
+                    wi[2 * k + 1] = a.y;
+                } else {
+#pragma unroll
+                    for (int q = 2 * k; q < 2 * k + 2; q++) {
+                        h[q] = kept_h[i][q];
+                        dy[q] = kept_dy[i][q];
+                        wi[q] = w[i][q];
+                    }
+                }
+            }
+        };
 #pragma unroll
         for (int i = 0; i < kNV; i++) {
-            pairs_of(rh[i], h[i]);
-            pairs_of(rg[i], dy[i]);
-        }
-        if (kAhead) fetch(row + groups < p.rows ? p.d : -V);
-#pragma unroll
-        for (int i = 0; i < kNV; i++) {
+            f2 h[P], dy[P], wi[P];
+            values(i, h, dy, wi);
 #pragma unroll
             for (int k = 0; k < P; k++) {
-                sq = fma2(h[i][k], h[i][k], sq);
-                dot = fma2(mul2(dy[i][k], w[i][k]), h[i][k], dot);
+                sq = fma2(h[k], h[k], sq);
+                dot = fma2(mul2(dy[k], wi[k]), h[k], dot);
             }
         }
         float a0, a1, b0, b1;
@@ -289,10 +333,18 @@ __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwd
         const float c = -r * r * r * (acc.y / (float)p.d);
         const f2 r2 = pack2(r, r), c2 = pack2(c, c);
         T* out = static_cast<T*>(p.dh) + (size_t)row * p.d;
+        if (kPastLate) fetch_past();
+        if (kWide && sizeof(T) == 2) {  // the 16 bits are turned into fp32 a second time rather than kept so
+#pragma unroll
+            for (int i = 0; i < kNV; i++)
+#pragma unroll
+                for (int k = 0; k < Raw<T, V>::kWords; k++) asm volatile("" : "+r"(rh[i].w[k]), "+r"(rg[i].w[k]));
+        }
 #pragma unroll
         for (int i = 0; i < kNV; i++) {
             const int at = place<V>(i, off);
-            f2 o[P];
+            f2 o[P], h[P], dy[P], wi[P];
+            values(i, h, dy, wi);
             if (ip)
                 pairs_of(past[i], o);
             else
@@ -300,10 +352,10 @@ __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwd
                 for (int k = 0; k < P; k++) o[k] = pack2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < P; k++) {
-                o[k] = fma2(c2, h[i][k], o[k]);
-                const f2 rdy = mul2(r2, dy[i][k]);
-                o[k] = fma2(rdy, w[i][k], o[k]);
-                dw[i][k] = fma2(rdy, h[i][k], dw[i][k]);
+                o[k] = fma2(c2, h[k], o[k]);
+                const f2 rdy = mul2(r2, dy[k]);
+                o[k] = fma2(rdy, wi[k], o[k]);
+                dw[i][k] = fma2(rdy, h[k], dw[i][k]);
             }
             if (at < d && at + V > 0) store_at<kShift, V>(out, at, d, o);
         }
@@ -336,7 +388,7 @@ struct Shape {
 };
 
 // Threads a row: those that hold it in `nv` vectors each, nv = 16 elements (one vector where a warp or a part
-// of one then holds the row, twice as many where 512 threads would not).  Rows of a warp or less share a block of
+// of one then holds the row, half as many again or twice as many where 512 threads would not).  Rows of a warp or less share a block of
 // 128 threads.  Blocks: `resident` threads on each of 148 SMs, or as many as there are rows; where rows start
 // inside a vector, rounded down to a multiple of 8.
 Shape shape_of(long long rows, int d, int es, int resident) {
@@ -345,7 +397,7 @@ Shape shape_of(long long rows, int d, int es, int resident) {
     if (vecs <= 32) {
         while (s.threads_x < vecs) s.threads_x *= 2;
     } else {
-        s.nv = vecs <= 512 * usual ? usual : (vecs <= 1024 * usual ? 2 * usual : 2 * usual + 1);
+        s.nv = vecs <= 512 * usual ? usual : vecs <= 768 * usual ? 3 * usual / 2 : vecs <= 1024 * usual ? 2 * usual : 2 * usual + 1;
         s.threads_x = ((vecs + s.nv - 1) / s.nv + 31) / 32 * 32;
     }
     if (s.threads_x <= 32) s.threads_y = 128 / s.threads_x;
@@ -372,6 +424,7 @@ cudaError_t by_vectors(int nv, int d, F f) {
     };
     if (nv == 1) return with(std::integral_constant<int, 1>{});
     if (nv == kUsual) return with(std::integral_constant<int, kUsual>{});
+    if (nv == 3 * kUsual / 2) return with(std::integral_constant<int, 3 * kUsual / 2>{});
     if (nv == 2 * kUsual) return with(std::integral_constant<int, 2 * kUsual>{});
     if (nv == 2 * kUsual + 1) return with(std::integral_constant<int, 2 * kUsual + 1>{});
     return cudaErrorInvalidValue;
@@ -409,7 +462,11 @@ cudaError_t launch_backward(const NormBwdParams& p, float* dweight, cudaStream_t
     const Shape s = backward_shape(p.rows, p.d, sizeof(T));
     const dim3 block(s.threads_x, s.threads_y);
     cudaError_t e = by_vectors<T>(s.nv, p.d, [&](auto nv, auto shift) {
-        ttt_rmsnorm_backward_kernel<T, decltype(nv)::value, decltype(shift)::value><<<(unsigned)s.blocks, block, 0, stream>>>(p);
+        const auto kernel = ttt_rmsnorm_backward_kernel<T, decltype(nv)::value, decltype(shift)::value>;
+        constexpr int kBytes = decltype(nv)::value * 16 / (int)sizeof(T) * 4;  // of the weight, a thread
+        const int smem = kBytes > 64 ? kBytes * s.threads_x : 0;
+        if (smem > 48 * 1024 - 8192 - 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        kernel<<<(unsigned)s.blocks, block, smem, stream>>>(p);
     });
     if (e != cudaSuccess) return e;
     return launch_column_sum((int)s.blocks, p.d, p.partial, dweight, stream);

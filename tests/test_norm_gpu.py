@@ -100,9 +100,10 @@ def test_backward(ttt, B, T, d, past, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
-@pytest.mark.parametrize("B,T,d", [(64, 300, 5), (8, 1000, 64), (3, 2000, 96), (1, 4000, 200)])
-def test_many_narrow_rows(ttt, B, T, d, kind):
-    """Several rows a block, and more rows than the blocks take at once."""
+@pytest.mark.parametrize("B,T,d", [(64, 300, 5), (8, 1000, 64), (3, 2000, 96), (1, 4000, 200), (1, 400, 9001),
+                                   (2, 170, 11000), (1, 300, 13004), (1, 310, 16383)])
+def test_many_rows(ttt, B, T, d, kind):
+    """Several narrow rows a block, rows that take most of an SM's registers, and more rows than the blocks take at once."""
     x, r, w = inputs(B, T, d, kind, True, seed=3)
     y, h = ttt.ttt_rmsnorm_forward(x.cuda(), w.cuda(), r.cuda())
     (yo, ye), (ho, he) = ob.rmsnorm(x, w, r)
