@@ -32,6 +32,7 @@ __device__ __forceinline__ int length_of(const int* lengths, int b, int T) {
 
 struct ConvParams {
     int T, C, piece, pieces, groups;  // groups: channel groups (blocks) a row
+    long long strips;                 // B pieces: what a thread walks of its channels
     long long ld;                     // elements from one row of x to the next
     const void *x, *state0;
     const float *weight, *bias;
@@ -41,6 +42,30 @@ struct ConvParams {
 
 constexpr int kThreads = 128;
 constexpr int kAhead = 4;  // rows on their way while the four before them are worked on
+
+// Blocks are kThreads columns (of one or four channels) of one strip, or of several where a row has fewer (kNarrow:
+// piece and sequence then differ from thread to thread, which costs registers that wide rows have no use for).
+inline dim3 block_of(int columns, bool narrow) {
+    int x = kThreads;
+    while (narrow && x > 8 && x / 2 >= columns) x /= 2;
+    return dim3(x, kThreads / x);
+}
+struct Place {
+    int column, piece, b;
+    bool on;
+};
+template <bool kNarrow>
+__device__ __forceinline__ Place place_of(int groups, int pieces, long long strips) {
+    const int grp = (int)(blockIdx.x % groups);
+    long long strip = blockIdx.x / groups;
+    if constexpr (kNarrow) strip = strip * blockDim.y + threadIdx.y;
+    Place at;
+    at.column = grp * (kNarrow ? (int)blockDim.x : kThreads) + (int)threadIdx.x;
+    at.on = !kNarrow || strip < strips;
+    at.piece = (int)(strip % pieces);
+    at.b = (int)(strip / pieces);
+    return at;
+}
 
 // Row t of the window of sequence b (t < 0: the state's rows), the thread's channels.
 template <typename T, int V, int W>
@@ -110,15 +135,12 @@ __device__ __forceinline__ void shift_in(f2 (&win)[W - 1][P], const f2 (&in)[P])
     }
 }
 
-template <typename T, int V, int W, bool kSilu>
+template <typename T, int V, int W, bool kSilu, bool kNarrow>
 __global__ void __launch_bounds__(kThreads, 6) ttt_conv_kernel(const ConvParams p) {
     constexpr int P = (V + 1) / 2;  // pairs
-    const long long block = blockIdx.x;
-    const int grp = (int)(block % p.groups);
-    const int piece = (int)(block / p.groups % p.pieces);
-    const int b = (int)(block / p.groups / p.pieces);
-    const int c = (grp * kThreads + threadIdx.x) * V;
-    if (c >= p.C) return;
+    const Place at = place_of<kNarrow>(p.groups, p.pieces, p.strips);
+    const int piece = at.piece, b = at.b, c = at.column * V;
+    if (c >= p.C || !at.on) return;
     const int n = length_of(p.lengths, b, p.T);
     const T* x = static_cast<const T*>(p.x) + (long long)b * p.T * p.ld + c;
     const T* state = p.state0 ? static_cast<const T*>(p.state0) + (long long)b * (W - 1) * p.C + c : nullptr;
@@ -193,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 6) ttt_conv_kernel(const ConvParams 
 
 struct ConvBwdParams {
     int T, C, piece, pieces, groups;
-    long long ld;
+    long long strips, ld;
     const void *x, *state0, *dy, *dstate_T;
     const float *weight, *bias;
     const int* lengths;
@@ -204,15 +226,12 @@ struct ConvBwdParams {
 constexpr int kBack = 4;     // rows of x and dy on their way
 constexpr int kBackVec = 4;  // channels a thread, where rows allow it
 
-template <typename T, int V, int W, bool kSilu>
+template <typename T, int V, int W, bool kSilu, bool kNarrow>
 __global__ void __launch_bounds__(kThreads, 4) ttt_conv_backward_kernel(const ConvBwdParams p) {
     constexpr int P = (V + 1) / 2;
-    const long long block = blockIdx.x;
-    const int grp = (int)(block % p.groups);
-    const int piece = (int)(block / p.groups % p.pieces);
-    const int b = (int)(block / p.groups / p.pieces);
-    const int c = (grp * kThreads + threadIdx.x) * V;
-    if (c >= p.C) return;
+    const Place at = place_of<kNarrow>(p.groups, p.pieces, p.strips);
+    const int piece = at.piece, b = at.b, c = at.column * V;
+    if (c >= p.C || !at.on) return;
     const int n = length_of(p.lengths, b, p.T);
 
     const f2 zero2 = pack2(0.f, 0.f), one2 = pack2(1.f, 1.f);
@@ -355,7 +374,7 @@ __global__ void __launch_bounds__(1024) ttt_conv_weight_sum_kernel(int rows, int
     const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y;
     float a = 0.f;
     if (c < C)
-#pragma unroll 4
+#pragma unroll 8
         for (int r = threadIdx.y; r < rows; r += 32) a += partial[((size_t)r * (W + 1) + j) * C + c];
     s[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
@@ -409,7 +428,11 @@ cudaError_t forward(const ConvArgs& a, cudaStream_t stream) {
     p.C = a.C;
     p.piece = forward_piece(a, v);
     p.pieces = a.T > 0 ? (a.T + p.piece - 1) / p.piece : 1;  // an empty sequence still passes its state on
-    p.groups = (a.C + kThreads * v - 1) / (kThreads * v);
+    const int columns = (a.C + v - 1) / v;
+    const bool narrow = columns <= kThreads / 2;
+    const dim3 threads = block_of(columns, narrow);
+    p.groups = (columns + threads.x - 1) / threads.x;
+    p.strips = (long long)a.B * p.pieces;
     p.ld = a.ld;
     p.x = a.x;
     p.state0 = a.state0;
@@ -418,15 +441,16 @@ cudaError_t forward(const ConvArgs& a, cudaStream_t stream) {
     p.lengths = a.lengths;
     p.y = a.y;
     p.state_T = a.state_T;
-    const long long blocks = (long long)a.B * p.pieces * p.groups;
+    const long long blocks = (p.strips + threads.y - 1) / threads.y * p.groups;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
     return by_width(a.W, a.silu, [&](auto w, auto silu) {
         constexpr int W = decltype(w)::value;
         constexpr bool kSilu = decltype(silu)::value;
+        const auto start = [&](auto kernel) { kernel<<<(unsigned)blocks, threads, 0, stream>>>(p); };
         if (vec)
-            ttt_conv_kernel<T, kV, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+            narrow ? start(ttt_conv_kernel<T, kV, W, kSilu, true>) : start(ttt_conv_kernel<T, kV, W, kSilu, false>);
         else
-            ttt_conv_kernel<T, 1, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+            narrow ? start(ttt_conv_kernel<T, 1, W, kSilu, true>) : start(ttt_conv_kernel<T, 1, W, kSilu, false>);
     });
 }
 
@@ -450,7 +474,11 @@ cudaError_t backward(const ConvBwdArgs& a, float* workspace, cudaStream_t stream
     p.C = a.f.C;
     p.piece = backward_piece(a.f.B, a.f.T, a.f.C, v);
     p.pieces = a.f.T > 0 ? (a.f.T + p.piece - 1) / p.piece : 1;
-    p.groups = (a.f.C + kThreads * v - 1) / (kThreads * v);
+    const int columns = (a.f.C + v - 1) / v;
+    const bool narrow = columns <= kThreads / 2;
+    const dim3 threads = block_of(columns, narrow);
+    p.groups = (columns + threads.x - 1) / threads.x;
+    p.strips = (long long)a.f.B * p.pieces;
     p.ld = a.f.ld;
     p.x = a.f.x;
     p.state0 = a.f.state0;
@@ -462,15 +490,16 @@ cudaError_t backward(const ConvBwdArgs& a, float* workspace, cudaStream_t stream
     p.dx = a.dx;
     p.dstate0 = a.dstate0;
     p.partial = workspace;
-    const long long blocks = (long long)a.f.B * p.pieces * p.groups;
+    const long long blocks = (p.strips + threads.y - 1) / threads.y * p.groups;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
     cudaError_t e = by_width(a.f.W, a.f.silu, [&](auto w, auto silu) {
         constexpr int W = decltype(w)::value;
         constexpr bool kSilu = decltype(silu)::value;
+        const auto start = [&](auto kernel) { kernel<<<(unsigned)blocks, threads, 0, stream>>>(p); };
         if (vec)
-            ttt_conv_backward_kernel<T, kV, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+            narrow ? start(ttt_conv_backward_kernel<T, kV, W, kSilu, true>) : start(ttt_conv_backward_kernel<T, kV, W, kSilu, false>);
         else
-            ttt_conv_backward_kernel<T, 1, W, kSilu><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+            narrow ? start(ttt_conv_backward_kernel<T, 1, W, kSilu, true>) : start(ttt_conv_backward_kernel<T, 1, W, kSilu, false>);
     });
     if (e != cudaSuccess) return e;
     ttt_conv_weight_sum_kernel<<<dim3((a.f.C + 31) / 32, a.f.W + 1), dim3(32, 32), 0, stream>>>(

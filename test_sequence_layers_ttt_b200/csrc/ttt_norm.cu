@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(1024) ttt_column_sum_kernel(int rows, int cols
     const int c = blockIdx.x * 32 + threadIdx.x;
     float a = 0.f;
     if (c < cols)
+#pragma unroll 8
         for (int r = threadIdx.y; r < rows; r += 32) a += partial[(size_t)r * cols + c];
     s[threadIdx.y][threadIdx.x] = a;
     __syncthreads();

@@ -1,4 +1,4 @@
-// Selective state space scan: the kernel for single tokens, and the choice among the kernels for prompts.
+// Selective state space scan: the kernel for single tokens and a few, and the choice among the kernels for prompts.
 //
 //   dt = softplus(dt_raw + dt_bias) (or dt_raw + dt_bias),  h_t = e^(dt_t A) h_{t-1} + dt_t u_t B_t,
 //   y_t = (sum_n C_t[n] h_t[n] + D u_t) silu(z_t)
@@ -40,7 +40,11 @@ __global__ void __launch_bounds__(128) ttt_ssm_token_kernel(const Params p) {
     const int n0 = part * kStates, live = on ? max(0, min(kStates, p.N - n0)) : 0;  // states that exist
     float h[kStates], a2[kStates];
     const size_t at = (size_t)bc * p.N + n0;
-    load_four<kVec>(p.h0 + at, live, h);
+    if (p.h0)
+        load_four<kVec>(p.h0 + at, live, h);
+    else
+        h[0] = h[1] = h[2] = h[3] = 0.f;
+    const int len = length_of(p.lengths, b, p.T);
     load_four<kVec>(p.A + (size_t)c * p.N + n0, live, a2);
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f, skip = on && p.D ? p.D[c] : 0.f;
 #pragma unroll
@@ -48,14 +52,16 @@ __global__ void __launch_bounds__(128) ttt_ssm_token_kernel(const Params p) {
     for (int t = 0; t < p.T; t++) {
         const long long row = (long long)b * p.T + t;
         float Bt[kStates], Ct[kStates], dt = 0.f, u = 0.f, z = 0.f;
-        load_four<kVec>(static_cast<const T*>(p.Bm) + row * p.ld_b + n0, live, Bt);
-        load_four<kVec>(static_cast<const T*>(p.Cm) + row * p.ld_c + n0, live, Ct);
-        if (on) {
+        const bool token = t < len;  // padding is not read, and a step of zero leaves the state
+        load_four<kVec>(static_cast<const T*>(p.Bm) + row * p.ld_b + n0, token ? live : 0, Bt);
+        load_four<kVec>(static_cast<const T*>(p.Cm) + row * p.ld_c + n0, token ? live : 0, Ct);
+        if (on && token) {
             dt = to_f32(static_cast<const T*>(p.dt)[row * p.ld_dt + c]) + bias;
             u = to_f32(static_cast<const T*>(p.u)[row * p.ld_u + c]);
             if (p.z) z = to_f32(static_cast<const T*>(p.z)[row * p.ld_z + c]);
         }
         if (p.softplus) dt = ssm::softplus(dt);
+        if (!token) dt = 0.f;
         const float du = dt * u;
         float y = 0.f;
 #pragma unroll
@@ -118,11 +124,14 @@ cudaError_t launch_ssm_token(const SsmArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_ssm_forward(const SsmArgs& a, cudaStream_t stream) {
+    // A few tokens take the tokens' kernel: up to 8, or 24 where the others would have more than 37 blocks, whose start and
+    // end cost as much as 24 tokens (14 x 7616 channels of 2 tokens 10 us against 74, of 24 tokens 50 against 76).
     // Blocks of 32 channels, one an SM.  Up to 37 of them (a quarter of 148 SMs) eight channels a block
     // still have an SM each, and those tiles, whose tokens are worked on side by side, take 61 clocks a
     // token against 87 (N = 16, bf16; 37 blocks of 4096 tokens: 132 us against 178).  Above 16 states the warps of a block
     // would hold too few registers for the other kernel.
     const long long blocks = (long long)a.B * ((a.C + 31) / 32);
+    if (a.T <= (blocks <= 37 ? 8 : 24)) return launch_ssm_token(a, stream);
     if (blocks <= 37) return launch_ssm_segments(a, 8, stream);
     return a.N <= 16 ? launch_ssm_scan(a, stream) : launch_ssm_segments(a, 32, stream);
 }

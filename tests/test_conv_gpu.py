@@ -60,6 +60,22 @@ def test_padded_batch(ttt, B, T, C, W, kind):
         assert not y[i, n[i]:].any()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,W", [(3, 1000, 8, 4), (5, 777, 3, 4), (2, 300, 64, 2), (3, 130, 250, 3), (7, 50, 12, 4)])
+def test_narrow_rows(ttt, B, T, C, W, kind):
+    """Few channels: a block takes several pieces of the tokens, of several sequences."""
+    x, w, b, s, g = inputs(B, T, C, W, kind)
+    n = bc.lengths_for(B, T, g)
+    dy, ds = bc.normal(g, B, T, C).to(x.dtype), bc.normal(g, B, W - 1, C).to(x.dtype)
+    y, st = ttt.ttt_conv_forward(x.cuda(), w.cuda(), up(b), up(s), lengths=n.cuda())
+    (yo, ye), so = ob.conv(x, w, b, s, n)
+    bc.close("y", y, yo, ye)
+    assert torch.equal(st.cpu().double(), so)
+    got = ttt.ttt_conv_backward(x.cuda(), w.cuda(), up(b), dy.cuda(), up(s), ds.cuda(), lengths=n.cuda())
+    for name, a, (v, e) in zip(("dx", "dweight", "dbias", "dstate0"), got, ob.conv_backward(x, w, b, dy, s, ds, n)):
+        bc.close(name, a, v, e)
+
+
 def test_lengths_outside_the_batch_are_taken_into_it(ttt):
     x, w, b, s, g = inputs(2, 9, 16, 4, "f32")
     y, st = ttt.ttt_conv_forward(x.cuda(), w.cuda(), up(b), up(s), lengths=torch.tensor([-3, 1000], dtype=torch.int32).cuda())

@@ -192,6 +192,25 @@ def test_few_rows_in_parts_with_the_state_in_place(ttt, B, C, N, kind):
     assert torch.equal(y, again[0]) and torch.equal(h, again[1])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,N", [(3, 1, 40, 16), (4, 8, 37, 5), (4, 9, 37, 5), (40, 24, 40, 16), (40, 25, 40, 16),
+                                     (40, 24, 33, 64), (40, 70, 36, 64), (39, 90, 33, 7)])
+def test_few_tokens_and_many_rows(ttt, B, T, C, N, kind):
+    """On both sides of the sizes at which another kernel takes the call: padded, with the state in place, and from zero."""
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=26)
+    n = bc.lengths_for(B, T, torch.Generator().manual_seed(27))
+    for b in range(B):
+        for k in ("u", "dt", "Bm", "Cm", "z"):
+            i[k][b, n[b]:] = NAN
+    c = bc.cuda(i)
+    y, h = forward(ttt, c, h_T=c["h0"], lengths=n.cuda())
+    check_forward((y, h), i, lengths=n)
+    for b in range(B):
+        assert not y[b, n[b]:].any()
+    i.pop("h0")
+    check_forward(forward(ttt, bc.cuda(i), lengths=n.cuda()), i, lengths=n)
+
+
 def test_few_rows_in_parts_of_growing_states(ttt):
     i = bc.ssm_inputs(1, 600, 20, 8, "f32", seed=24, softplus=False)
     i["A"] = -0.02 * i["A"]
