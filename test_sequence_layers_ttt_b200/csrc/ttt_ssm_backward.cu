@@ -527,44 +527,47 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
 }
 
 // ---------------------------------------------------------------- the sums over blocks and sequences
-__global__ void __launch_bounds__(256) ttt_ssm_bc_sum_kernel(int B, int T, int N, int cblocks, const int* lengths,
-                                                             const float* __restrict__ part, float* __restrict__ dB,
-                                                             float* __restrict__ dC) {
-    const size_t per = (size_t)T * 2 * N, total = (size_t)B * per;
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const int b = (int)(i / per);
-    const size_t r = i % per;
-    const int t = (int)(r / (2 * N)), m = (int)(r % (2 * N));
-    float a = 0.f;
-    if (t < length_of(lengths, b, T))
-        for (int k = 0; k < cblocks; k++) a += part[(size_t)k * total + i];
-    (m < N ? dB : dC)[((size_t)b * T + t) * N + (m < N ? m : m - N)] = a;
-}
-
-// 32 columns a block; its eight warps share out the rows
-__global__ void __launch_bounds__(256) ttt_ssm_channel_sum_kernel(int rows, int C, int N, const float* __restrict__ part,
-                                                                  float* __restrict__ dA, float* __restrict__ dD,
-                                                                  float* __restrict__ dbias) {
+struct SsmSums {
+    int B, T, C, N, cblocks, rows;  // rows: parts of sequences
+    unsigned bc_blocks;             // blocks that sum dB and dC; the others sum dA, dD and ddt_bias
+    const int* lengths;
+    const float *part_bc, *part_c;
+    float *dB, *dC, *dA, *dD, *dbias;
+};
+__global__ void __launch_bounds__(256) ttt_ssm_sum_kernel(const SsmSums p) {
     __shared__ double sums[8][32];
+    if (blockIdx.x < p.bc_blocks) {
+        const size_t per = (size_t)p.T * 2 * p.N, total = (size_t)p.B * per;
+        const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+        if (i >= total) return;
+        const int b = (int)(i / per);
+        const size_t r = i % per;
+        const int t = (int)(r / (2 * p.N)), m = (int)(r % (2 * p.N));
+        float a = 0.f;
+        if (t < length_of(p.lengths, b, p.T))
+            for (int k = 0; k < p.cblocks; k++) a += p.part_bc[(size_t)k * total + i];
+        (m < p.N ? p.dB : p.dC)[((size_t)b * p.T + t) * p.N + (m < p.N ? m : m - p.N)] = a;
+        return;
+    }
+    // 32 columns a block; its eight warps share out the rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const size_t cols = (size_t)(N + 2) * C, i = (size_t)blockIdx.x * 32 + lane;
+    const size_t cols = (size_t)(p.N + 2) * p.C, i = (size_t)(blockIdx.x - p.bc_blocks) * 32 + lane;
     double a = 0.0;
     if (i < cols) {
 #pragma unroll 4
-        for (int r = warp; r < rows; r += 8) a += part[(size_t)r * cols + i];
+        for (int r = warp; r < p.rows; r += 8) a += p.part_c[(size_t)r * cols + i];
     }
     sums[warp][lane] = a;
     __syncthreads();
     if (warp != 0 || i >= cols) return;
     for (int k = 1; k < 8; k++) a += sums[k][lane];
-    const int n = (int)(i / C), c = (int)(i % C);
-    if (n < N)
-        dA[(size_t)c * N + n] = (float)a;
-    else if (n == N) {
-        if (dD) dD[c] = (float)a;
-    } else if (dbias) {
-        dbias[c] = (float)a;
+    const int n = (int)(i / p.C), c = (int)(i % p.C);
+    if (n < p.N)
+        p.dA[(size_t)c * p.N + n] = (float)a;
+    else if (n == p.N) {
+        if (p.dD) p.dD[c] = (float)a;
+    } else if (p.dbias) {
+        p.dbias[c] = (float)a;
     }
 }
 
@@ -575,8 +578,8 @@ constexpr int chunk_for(int kNW) { return kNW <= 8 ? 16 : 8; }
 // Parts of the time axis.  A launch of few blocks waits on its own results, some 600 clocks a token.  So where the blocks
 // fill at most half of the places that the SMs have for them, the axis is split into as many parts as there are
 // places for, whole tiles each and at most 64, which is what the walk over the parts' ends costs.  Measured, split
-// against whole (bf16, 16 states, 444 places): 4 blocks of 2641 tokens 60 us against 898, 36 of 614 77 against 320,
-// 128 of 1024 242 against 363, 192 of 1024 348 against 414.
+// against whole (bf16, 16 states, 444 places): 4 blocks of 2641 tokens 58 us against 898, 36 of 614 68 against 320,
+// 128 of 1024 241 against 363, 192 of 1024 345 against 414.
 struct Split {
     int segs, seg_len;
 };
@@ -698,16 +701,11 @@ cudaError_t launch_ssm_backward(const SsmBwdArgs& a, float* workspace, cudaStrea
     p.vec_bc = rows16(f.Bm, f.ld_b, f.N, es) && rows16(f.Cm, f.ld_c, f.N, es);
     cudaError_t e = f.dtype == TTT_BF16 ? dispatch<__nv_bfloat16>(p, stream) : dispatch<float>(p, stream);
     if (e != cudaSuccess) return e;
-    const size_t bc = (size_t)f.B * f.T * 2 * f.N;
-    if (bc > 0) {
-        ttt_ssm_bc_sum_kernel<<<(unsigned)((bc + 255) / 256), 256, 0, stream>>>(f.B, f.T, f.N, p.cblocks, f.lengths,
-                                                                                p.part_bc, a.dB, a.dC);
-        e = cudaPeekAtLastError();
-        if (e != cudaSuccess) return e;
-    }
-    const size_t ch = (size_t)(f.N + 2) * f.C;
-    ttt_ssm_channel_sum_kernel<<<(unsigned)((ch + 31) / 32), 256, 0, stream>>>(f.B * p.segs, f.C, f.N, p.part_c, a.dA, a.dD,
-                                                                                a.ddt_bias);
+    const size_t bc = ((size_t)f.B * f.T * 2 * f.N + 255) / 256, ch = ((size_t)(f.N + 2) * f.C + 31) / 32;
+    if (bc + ch >= (1ULL << 31)) return cudaErrorInvalidValue;
+    const SsmSums sums{f.B, f.T, f.C, f.N, p.cblocks, f.B * p.segs, (unsigned)bc, f.lengths,
+                       p.part_bc, p.part_c, a.dB, a.dC, a.dA, a.dD, a.ddt_bias};
+    ttt_ssm_sum_kernel<<<(unsigned)(bc + ch), 256, 0, stream>>>(sums);
     return cudaPeekAtLastError();
 }
 
