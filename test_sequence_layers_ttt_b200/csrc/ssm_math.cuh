@@ -68,8 +68,9 @@ __device__ __forceinline__ void decays(float (&a)[2 * kPairs], const f2 (&x)[kPa
     }
 }
 
-// a v + e; 0 becomes e where the decay over many tokens, of a growing state, has overflowed
-__device__ __forceinline__ float carried(float v, float a, float e) { return v == 0.f ? e : fmaf(a, v, e); }
+// v carried over many tokens, v a + e.  A growing state's a may pass the largest float where v a does not, so it comes
+// as two factors of about its root; where they overflow too, a v of zero still becomes e.
+__device__ __forceinline__ float carried(float v, float a0, float a1, float e) { return v == 0.f ? e : fmaf(a0 * v, a1, e); }
 
 __device__ __forceinline__ int length_of(const int* lengths, int b, int T) {
     if (!lengths) return T;

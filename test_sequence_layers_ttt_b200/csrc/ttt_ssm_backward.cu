@@ -44,7 +44,7 @@ struct SsmBwdParams {
     float* ckpt;     // [B][chunks][4 kNW][C]
     float* part_bc;  // [cblocks][B][T][2][N]
     float* part_c;   // [B][segs][N + 2][C]: dA, dD, ddt_bias
-    float* carry;    // [B][segs][3][4 kNW][C]: a part's end state from zero, its gradient to the part before, its decay
+    float* carry;    // [B][segs][4][4 kNW][C]: a part's end state from zero, its gradient to the part before, its decay in two factors
     bool vec_rows, vec_bc;
 };
 
@@ -64,33 +64,36 @@ __device__ __forceinline__ Where where(const SsmBwdParams& p) {
     w.len = max(min(length_of(p.lengths, w.b, p.T) - w.t0, w.T), 0);
     return w;
 }
-// Carry value m (0: state, 1: gradient, 2: decay) of part seg, of the thread's first state n0 and channel c
+// Carry value m (0: state, 1: gradient, 2 and 3: the decay's factors) of part seg, of the thread's first state n0 and channel c
 template <int kNp>
 __device__ __forceinline__ size_t carry_at(const SsmBwdParams& p, int b, int seg, int m, int n0, int c) {
-    return ((((size_t)b * p.segs + seg) * 3 + m) * kNp + n0) * p.C + c;
+    return ((((size_t)b * p.segs + seg) * 4 + m) * kNp + n0) * p.C + c;
 }
 // v folded over `count` parts from part `from` on, in steps of `by`; m as in carry_at.  Eight parts' values are on
-// their way at a time: one by one, 64 parts took longer than a walk along one of them.
+// their way at a time (four where a thread has 128 registers): one by one, 64 parts took longer than a walk along one of them.
 template <int kNp>
 __device__ __forceinline__ void fold(float (&v)[kStates], const SsmBwdParams& p, int b, int from, int by, int count, int m,
                                      int n0, int c) {
-    for (int j0 = 0; j0 < count; j0 += 8) {
-        float e[8][kStates], a[8][kStates];
+    constexpr int kBatch = kNp > 16 ? 4 : 8;
+    for (int j0 = 0; j0 < count; j0 += kBatch) {
+        float e[kBatch][kStates], a0[kBatch][kStates], a1[kBatch][kStates];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
+        for (int j = 0; j < kBatch; j++) {
             const bool live = j0 + j < count;
             const int seg = live ? from + (j0 + j) * by : 0;
-            const float *pe = p.carry + carry_at<kNp>(p, b, seg, m, n0, c), *pa = p.carry + carry_at<kNp>(p, b, seg, 2, n0, c);
+            const float *pe = p.carry + carry_at<kNp>(p, b, seg, m, n0, c), *p0 = p.carry + carry_at<kNp>(p, b, seg, 2, n0, c);
+            const float* p1 = p.carry + carry_at<kNp>(p, b, seg, 3, n0, c);
 #pragma unroll
             for (int i = 0; i < kStates; i++) {
                 e[j][i] = live ? pe[(size_t)i * p.C] : 0.f;
-                a[j][i] = live ? pa[(size_t)i * p.C] : 1.f;
+                a0[j][i] = live ? p0[(size_t)i * p.C] : 1.f;
+                a1[j][i] = live ? p1[(size_t)i * p.C] : 1.f;
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; j++)
+        for (int j = 0; j < kBatch; j++)
 #pragma unroll
-            for (int i = 0; i < kStates; i++) v[i] = carried(v[i], a[j][i], e[j][i]);
+            for (int i = 0; i < kStates; i++) v[i] = carried(v[i], a0[j][i], a1[j][i], e[j][i]);
     }
 }
 
@@ -111,7 +114,7 @@ struct CkptSmem {
 
 // kK: tokens of a chunk; a tile is two chunks.  kEnds: a part of the time axis for itself, as carry has it.
 // The gradient that leaves a part to the one before is sum_t (a_first ... a_t) C_t dy'_t, so it too is
-// summed walking forwards.
+// summed walking forwards; the product of the even tokens' decays and that of the odd ones' are kept apart, as carried() takes them.
 template <typename T, int kNW, int kK, bool kEnds>
 __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmBwdParams p) {
     constexpr int kNp = kStates * kNW, kTile = 2 * kK, kThreads = 32 * kNW;
@@ -124,14 +127,14 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
     const int len = w.len;
     const int n_chunks = (len + kK - 1) / kK, tiles = (len + kTile - 1) / kTile;
     const int n0 = warp * kStates;
-    float h[kStates], a2[kStates], back[kStates], all[kStates];
+    float h[kStates], a2[kStates], back[kStates], all[2][kStates];
 #pragma unroll
     for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N;
         a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
         h[i] = !kEnds && live && p.h0 ? p.h0[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
         back[i] = 0.f;
-        all[i] = 1.f;
+        all[0][i] = all[1][i] = 1.f;
     }
     if (!kEnds && on) fold<kNp>(h, p, w.b, 0, 1, w.seg, 0, n0, c);
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f;
@@ -234,8 +237,8 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
                         unpack2(mul2(dy[2 * q + 1], Cq.y), g[2], g[3]);
 #pragma unroll
                         for (int k = 0; k < 4; k++) {
-                            all[i] *= a[4 * q + k];
-                            back[i] = carried(g[k], all[i], back[i]);
+                            all[k & 1][i] *= a[4 * q + k];
+                            back[i] = carried(g[k], all[0][i], all[1][i], back[i]);
                         }
                     }
                 }
@@ -247,7 +250,8 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
         for (int i = 0; i < kStates; i++) {
             p.carry[carry_at<kNp>(p, w.b, w.seg, 0, n0 + i, c)] = h[i];
             p.carry[carry_at<kNp>(p, w.b, w.seg, 1, n0 + i, c)] = back[i];
-            p.carry[carry_at<kNp>(p, w.b, w.seg, 2, n0 + i, c)] = all[i];
+            p.carry[carry_at<kNp>(p, w.b, w.seg, 2, n0 + i, c)] = all[0][i];
+            p.carry[carry_at<kNp>(p, w.b, w.seg, 3, n0 + i, c)] = all[1][i];
         }
     }
 }
@@ -605,7 +609,7 @@ Layout layout(int B, int T, int C, int N) {
     l.part_bc = up(cblocks * B * T * 2 * N);
     const size_t segs = (size_t)split_of(B, T, C, N).segs;
     l.part_c = up(B * segs * (N + 2) * C);
-    l.carry = segs > 1 ? up(B * segs * 3 * kStates * nw * C) : 0;
+    l.carry = segs > 1 ? up(B * segs * 4 * kStates * nw * C) : 0;
     l.total = l.ckpt + l.part_bc + l.part_c + l.carry;
     return l;
 }

@@ -26,7 +26,7 @@ constexpr int kMaxWarps = 8;  // 128 tokens a tile; a thread's 64 decays and 64 
 // B and C as floats, A log2(e), the state that goes from tile to tile, the segments' ends and decays.
 template <typename T, int kL>
 struct SegSmem {
-    float4 *end, *fall;  // [2][kMaxWarps][32]
+    float4 *end, *fall;  // [2][kMaxWarps][32]; fall: the decays or their roots
     float4 *a2, *h;      // [groups][32]; [2][groups][32]
     float *b, *c;        // [n_pad][tile + 4]: a state's tokens side by side
     T *u, *dt, *z;       // [2][tile][kL]
@@ -181,8 +181,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
                     }
                 }
                 s.end[(turn * kMaxWarps + warp) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
+                // The same for all warps.  Decays of states that grow are left as their roots, as carried() takes them; for the
+                // others, where its product and comparison a state and segment cost 6 %, as they are.
+                const bool grows = !p.softplus || __any_sync(0xffffffffu, fmaxf(fmaxf(a2[0], a2[1]), fmaxf(a2[2], a2[3])) > 0.f);
+                const float fall_dt = grows ? 0.5f * sum_dt : sum_dt;
                 s.fall[(turn * kMaxWarps + warp) * 32 + lane] =
-                    make_float4(decay(sum_dt * a2[0]), decay(sum_dt * a2[1]), decay(sum_dt * a2[2]), decay(sum_dt * a2[3]));
+                    make_float4(decay(fall_dt * a2[0]), decay(fall_dt * a2[1]), decay(fall_dt * a2[2]), decay(fall_dt * a2[3]));
                 __syncthreads();
                 const float4 first = s.h[(buf * groups + g) * 32 + lane];
                 h[0] = first.x;
@@ -191,10 +195,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
                 h[3] = first.w;
                 for (int v = 0; v < warp + (ends ? 1 : 0); v++) {
                     const float4 e = s.end[(turn * kMaxWarps + v) * 32 + lane], f = s.fall[(turn * kMaxWarps + v) * 32 + lane];
-                    h[0] = fmaf(f.x, h[0], e.x);
-                    h[1] = fmaf(f.y, h[1], e.y);
-                    h[2] = fmaf(f.z, h[2], e.z);
-                    h[3] = fmaf(f.w, h[3], e.w);
+                    if (grows) {
+                        h[0] = carried(h[0], f.x, f.x, e.x);
+                        h[1] = carried(h[1], f.y, f.y, e.y);
+                        h[2] = carried(h[2], f.z, f.z, e.z);
+                        h[3] = carried(h[3], f.w, f.w, e.w);
+                    } else {
+                        h[0] = fmaf(f.x, h[0], e.x);
+                        h[1] = fmaf(f.y, h[1], e.y);
+                        h[2] = fmaf(f.z, h[2], e.z);
+                        h[3] = fmaf(f.w, h[3], e.w);
+                    }
                 }
                 if (ends) {
                     if (warp == warps - 1) s.h[((buf ^ 1) * groups + g) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
@@ -266,6 +277,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
             __syncthreads();
             float total = 0.f;
             for (int v = 0; v < warps; v++) total += sums[v * 32 + lane];
+            total *= 0.5f;
             __syncthreads();
             for (int g = warp; g < groups; g += warps) {
                 const float4 A4 = s.a2[g * 32 + lane];
@@ -278,7 +290,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
                 float4 h = cluster.map_shared_rank(s.end, 0)[g * 32 + lane];
                 for (int r = 1; r < rank; r++) {
                     const float4 e = cluster.map_shared_rank(s.end, r)[g * 32 + lane], f = cluster.map_shared_rank(s.fall, r)[g * 32 + lane];
-                    h = make_float4(carried(h.x, f.x, e.x), carried(h.y, f.y, e.y), carried(h.z, f.z, e.z), carried(h.w, f.w, e.w));
+                    h = make_float4(carried(h.x, f.x, f.x, e.x), carried(h.y, f.y, f.y, e.y), carried(h.z, f.z, f.z, e.z), carried(h.w, f.w, f.w, e.w));
                 }
                 s.h[(buf * groups + g) * 32 + lane] = h;
             }

@@ -222,6 +222,47 @@ def test_few_rows_in_parts_of_growing_states(ttt):
     assert not y.any() and not h.any()
 
 
+def growing(B, T, C, N, steps, state=0.0, seed=28):
+    """States that grow by e^steps[t] a token, fed by nothing; `state`: the first one's size."""
+    i = bc.ssm_inputs(B, T, C, N, "f32", seed=seed, softplus=False)
+    i["A"], i["dt_bias"] = torch.ones(C, N), torch.zeros(C)
+    i["dt"] = steps[None, :, None].expand(B, T, C).contiguous()
+    i["u"], i["h0"] = torch.zeros(B, T, C), state * i["h0"]
+    return i
+
+
+# the kernels for a few tokens, for few channels (one block a row, and a cluster), for more, and for many states
+@pytest.mark.parametrize("B,T,C,N", [(1, 8, 9, 16), (1, 60, 9, 16), (1, 700, 8, 5), (40, 60, 9, 16), (40, 60, 9, 20), (20, 300, 9, 33)])
+def test_growth_that_overflows_over_tokens_of_an_empty_state(ttt, B, T, C, N):
+    """e^6 a token: nothing before the last tokens' inputs, and nothing but zeros without them."""
+    i = growing(B, T, C, N, torch.full((T,), 6.0))
+    y, h = forward(ttt, bc.cuda(i), dt_softplus=False)
+    assert not y.any() and not h.any()
+    i["u"][:, -5:] = bc.normal(torch.Generator().manual_seed(29), B, 5, C)
+    check_forward(forward(ttt, bc.cuda(i), dt_softplus=False), i, softplus=False)
+
+
+@pytest.mark.parametrize("B,T,C,N,step,at", [(1, 26, 9, 16, 5.6, (0, 26)), (40, 26, 9, 20, 5.6, (0, 26)), (40, 26, 9, 16, 5.6, (0, 26)),
+                                             (1, 1024, 8, 5, 0.7, (128, 300))])
+def test_growth_that_overflows_over_tokens_of_a_tiny_state(ttt, B, T, C, N, step, at):
+    """A state of 1e-30 grows into ordinary numbers, though its decay over a piece of the tokens passes the largest float."""
+    steps = torch.zeros(T)
+    steps[slice(*at)] = step
+    i = growing(B, T, C, N, steps, state=1e-30)
+    check_forward(forward(ttt, bc.cuda(i), dt_softplus=False), i, softplus=False)
+
+
+def test_backward_of_growth_that_overflows_over_a_part(ttt):
+    """The time axis in parts of 32 tokens: e^3 a token over the first 40, then a state that stays."""
+    B, T, C, N = 1, 2048, 8, 4
+    steps = torch.zeros(T)
+    steps[:40] = 3.0
+    i = growing(B, T, C, N, steps, state=1e-30)
+    dy = torch.zeros(B, T, C)
+    dy[:, -1] = 1e-30
+    check_backward(backward(ttt, bc.cuda(i), dy.cuda(), dt_softplus=False), i, dy, None, softplus=False)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,C,N", SIZES)
 def test_backward(ttt, B, T, C, N, kind):
