@@ -139,7 +139,7 @@ def _steps(u, dt, A, Bm, dt_bias, softplus, live):
     step, step_err, u = (torch.where(keep, v, 0.0) for v in (step, step_err, u))
     x = (step[..., None] * A).abs() / math.log(2)
     a = torch.exp(step[..., None] * A)
-    near = torch.where(x < 0.0625, 1.3e-7 * x + torch.where(A > 0, 1e-5 * x, 0.0) + 2 * U, 2.0 ** -22 + 2 * U)
+    near = torch.where(x < 0.0625, 1.3e-7 * x + 2 * U, 2.0 ** -22 + 2 * U)
     a_err = a * (step_err[..., None] * A.abs() + 3 * U * x + near)
     du, du_err = step * u, (step_err + U * step.abs()) * u.abs()
     Bm = torch.where(keep, Bm, 0.0)

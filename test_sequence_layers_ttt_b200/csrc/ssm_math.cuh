@@ -4,11 +4,14 @@
 // 1 / |x| tokens, so an error of a that does not average out grows by that factor; the special-function
 // unit's 2^x is off by up to 2^-22 and, between -1/16 and 0, by 2.5e-8 low on average (measured over
 // 2^20 points an octave).  So for |x| < 1/16 the decay is 1 + x q(x) with q the quadratic that fits
-// (2^x - 1) / x on [-1/16, 0] to 1.3e-7 (Remez exchange; within 1e-5 up to +1/16, for a state that
-// grows): 1 - a is then right to 1.3e-7 whatever its size, and only the last rounding, which is to
+// (2^x - 1) / x on [-1/16, 0] to 1.3e-7 (Remez exchange), or, where x may be positive, the cubic that fits it
+// on [-1/16, 1/16] to 1e-8 (interpolation at the zeros of a Chebyshev polynomial; the quadratic is off by 1e-5
+// at +1/16): 1 - a is then right to 1.3e-7 whatever its size, and only the last rounding, which is to
 // nearest, is left.  Beyond it the unit's result stands: its error counts at most 16 times there.
-// The cost is three of the pipe's fused multiply-adds a state beside one special-function result
-// (16 a clock an SM), which stays the bound.
+// The cost is three or four of the pipe's fused multiply-adds a state beside one special-function result
+// (16 a clock an SM), which stays the bound.  With the cubic for all states the scan of many channels took 1456 us
+// against 1414 (1.3B width, 32k tokens), so there a warp asks once whether any of its states grows; elsewhere it is used
+// for all (gradient of 8 x 2048 x 1536: 1.02 ms against 1.00).
 #pragma once
 
 #include "vec_io.cuh"
@@ -18,10 +21,11 @@ namespace ssm {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSmall = 0.0625f;
-constexpr float kQ0 = 0x1.62e42ep-1f, kQ1 = 0x1.ebf0e6p-3f, kQ2 = 0x1.bf5dd8p-5f;
+constexpr float kQ0 = 0x1.62e42ep-1f, kQ1 = 0x1.ebf0e6p-3f, kQ2 = 0x1.bf5dd8p-5f;                              // x <= 0
+constexpr float kG0 = 0x1.62e430p-1f, kG1 = 0x1.ebfbe0p-3f, kG2 = 0x1.c6bb7ap-5f, kG3 = 0x1.3b2fc4p-7f;  // any x
 
 __device__ __forceinline__ float decay(float x) {
-    const float q = fmaf(fmaf(kQ2, x, kQ1), x, kQ0);
+    const float q = fmaf(fmaf(fmaf(kG3, x, kG2), x, kG1), x, kG0);
     const float near_one = fmaf(q, x, 1.f);
     return fabsf(x) < kSmall ? near_one : ex2(x);
 }
@@ -46,16 +50,27 @@ __device__ __forceinline__ void ex2_beyond(float& near_one, float x) {
         : "+f"(near_one)
         : "f"(x));
 }
-// decay() of 2 kPairs values, x in pairs; step by step over all pairs, so that a warp has independent work
-// at every step
-template <int kPairs>
+// Whether any state of the warp may have a positive x
+__device__ __forceinline__ bool warp_grows(bool softplus, const float (&a2)[4]) {
+    return __any_sync(0xffffffffu, !softplus || fmaxf(fmaxf(a2[0], a2[1]), fmaxf(a2[2], a2[3])) > 0.f);
+}
+
+// decay() of 2 kPairs values, x in pairs, all x <= 0 unless kGrow; step by step over all pairs, so that a warp has
+// independent work at every step
+template <bool kGrow, int kPairs>
 __device__ __forceinline__ void decays(float (&a)[2 * kPairs], const f2 (&x)[kPairs]) {
-    const f2 c2 = pack2(kQ2, kQ2), c1 = pack2(kQ1, kQ1), c0 = pack2(kQ0, kQ0), one = pack2(1.f, 1.f);
+    const auto step = [&](f2(&q)[kPairs], float c) {
+        const f2 c2 = pack2(c, c);
+#pragma unroll
+        for (int i = 0; i < kPairs; i++) q[i] = fma2(q[i], x[i], c2);
+    };
+    const f2 one = pack2(1.f, 1.f), top = kGrow ? pack2(kG3, kG3) : pack2(kQ2, kQ2);
     f2 q[kPairs];
 #pragma unroll
-    for (int i = 0; i < kPairs; i++) q[i] = fma2(c2, x[i], c1);
-#pragma unroll
-    for (int i = 0; i < kPairs; i++) q[i] = fma2(q[i], x[i], c0);
+    for (int i = 0; i < kPairs; i++) q[i] = top;
+    if (kGrow) step(q, kG2);
+    step(q, kGrow ? kG1 : kQ1);
+    step(q, kGrow ? kG0 : kQ0);
 #pragma unroll
     for (int i = 0; i < kPairs; i++) q[i] = fma2(q[i], x[i], one);
 #pragma unroll

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
                 float a[4 * kQ];
 #pragma unroll
                 for (int k = 0; k < 2 * kQ; k++) x[k] = mul2(dt[k], A2);
-                decays<2 * kQ>(a, x);
+                decays<true>(a, x);
                 const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][half * kK]);
 #pragma unroll
                 for (int q = 0; q < kQ; q++) {
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
                 f2 x[2 * kQ];
 #pragma unroll
                 for (int k = 0; k < 2 * kQ; k++) x[k] = mul2(dt[k], A2);
-                decays<2 * kQ>(a[i], x);
+                decays<true>(a[i], x);
                 const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][0]);
                 float h = start[i] = first[i];
 #pragma unroll

@@ -12,6 +12,8 @@
 // waits on its own results: two channels a thread would hide that but leave half of the SMs idle.
 #include "ssm_params.cuh"
 
+#include <type_traits>
+
 namespace ttt {
 namespace {
 
@@ -136,6 +138,51 @@ __global__ void __launch_bounds__(32 * (kWarps + kHelpers)) ttt_ssm_scan_kernel(
         a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
         h[i] = live && p.h0 ? p.h0[((size_t)b * p.C + c) * p.N + n0 + i] : 0.f;
     }
+    // the recursion over tile m
+    const bool grows = warp_grows(p.softplus, a2);
+    const auto walk = [&](int m, auto grow) {
+        const int buf = m & 1;
+        constexpr int kAt = 4;  // quads in work at once
+        for (int q0 = 0; q0 < kQuads; q0 += kAt) {
+            f2 dt[2 * kAt], du[2 * kAt], y[2 * kAt];
+#pragma unroll
+            for (int q = 0; q < kAt; q++) {
+                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s.dt[(buf * kQuads + q0 + q) * 32 + lane]);
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(&s.du[(buf * kQuads + q0 + q) * 32 + lane]);
+                dt[2 * q] = d.x;
+                dt[2 * q + 1] = d.y;
+                du[2 * q] = e.x;
+                du[2 * q + 1] = e.y;
+            }
+#pragma unroll
+            for (int i = 0; i < kStates; i++) {
+                const f2 A2 = pack2(a2[i], a2[i]);
+                f2 x[2 * kAt];
+                float a[4 * kAt];
+#pragma unroll
+                for (int k = 0; k < 2 * kAt; k++) x[k] = mul2(dt[k], A2);
+                decays<decltype(grow)::value>(a, x);
+                const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[(buf * kNp + n0 + i) * kPitch + 4 * q0]);
+                const ulonglong2* Ci = reinterpret_cast<const ulonglong2*>(&s.c[(buf * kNp + n0 + i) * kPitch + 4 * q0]);
+#pragma unroll
+                for (int q = 0; q < kAt; q++) {
+                    const ulonglong2 Bq = Bi[q], Cq = Ci[q];
+                    const f2 in[2] = {mul2(du[2 * q], Bq.x), mul2(du[2 * q + 1], Bq.y)}, out[2] = {Cq.x, Cq.y};
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        float lo, hi;
+                        unpack2(in[k], lo, hi);
+                        lo = fmaf(a[4 * q + 2 * k], h[i], lo);
+                        h[i] = hi = fmaf(a[4 * q + 2 * k + 1], lo, hi);
+                        y[2 * q + k] = i == 0 ? mul2(out[k], pack2(lo, hi)) : fma2(out[k], pack2(lo, hi), y[2 * q + k]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kAt; q++)
+                *reinterpret_cast<ulonglong2*>(&s.y[((buf * kWarps + warp) * kQuads + q0 + q) * 32 + lane]) = make_ulonglong2(y[2 * q], y[2 * q + 1]);
+        }
+    };
     const int tiles = (len + kTile - 1) / kTile;
     // all but the newest of the copies have come in, for all helpers
     const auto arrived = [&](bool newest_too) {
@@ -161,47 +208,7 @@ __global__ void __launch_bounds__(32 * (kWarps + kHelpers)) ttt_ssm_scan_kernel(
                 prepare(m + 1);
             }
         } else if (m < tiles) {
-            const int buf = m & 1;
-            constexpr int kAt = 4;  // quads in work at once
-            for (int q0 = 0; q0 < kQuads; q0 += kAt) {
-                f2 dt[2 * kAt], du[2 * kAt], y[2 * kAt];
-#pragma unroll
-                for (int q = 0; q < kAt; q++) {
-                    const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&s.dt[(buf * kQuads + q0 + q) * 32 + lane]);
-                    const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(&s.du[(buf * kQuads + q0 + q) * 32 + lane]);
-                    dt[2 * q] = d.x;
-                    dt[2 * q + 1] = d.y;
-                    du[2 * q] = e.x;
-                    du[2 * q + 1] = e.y;
-                }
-#pragma unroll
-                for (int i = 0; i < kStates; i++) {
-                    const f2 A2 = pack2(a2[i], a2[i]);
-                    f2 x[2 * kAt];
-                    float a[4 * kAt];
-#pragma unroll
-                    for (int k = 0; k < 2 * kAt; k++) x[k] = mul2(dt[k], A2);
-                    decays<2 * kAt>(a, x);
-                    const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[(buf * kNp + n0 + i) * kPitch + 4 * q0]);
-                    const ulonglong2* Ci = reinterpret_cast<const ulonglong2*>(&s.c[(buf * kNp + n0 + i) * kPitch + 4 * q0]);
-#pragma unroll
-                    for (int q = 0; q < kAt; q++) {
-                        const ulonglong2 Bq = Bi[q], Cq = Ci[q];
-                        const f2 in[2] = {mul2(du[2 * q], Bq.x), mul2(du[2 * q + 1], Bq.y)}, out[2] = {Cq.x, Cq.y};
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            float lo, hi;
-                            unpack2(in[k], lo, hi);
-                            lo = fmaf(a[4 * q + 2 * k], h[i], lo);
-                            h[i] = hi = fmaf(a[4 * q + 2 * k + 1], lo, hi);
-                            y[2 * q + k] = i == 0 ? mul2(out[k], pack2(lo, hi)) : fma2(out[k], pack2(lo, hi), y[2 * q + k]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < kAt; q++)
-                    *reinterpret_cast<ulonglong2*>(&s.y[((buf * kWarps + warp) * kQuads + q0 + q) * 32 + lane]) = make_ulonglong2(y[2 * q], y[2 * q + 1]);
-            }
+            grows ? walk(m, std::true_type{}) : walk(m, std::false_type{});
         }
         __syncthreads();
     }

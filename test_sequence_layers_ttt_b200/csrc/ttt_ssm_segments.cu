@@ -12,6 +12,7 @@
 #include "ssm_params.cuh"
 
 #include <cooperative_groups.h>
+#include <type_traits>
 
 namespace ttt {
 namespace {
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
                     f2 x[kSeg / 2];
 #pragma unroll
                     for (int k = 0; k < kSeg / 2; k++) x[k] = mul2(dt2[k], A2);
-                    decays<kSeg / 2>(a[i], x);
+                    decays<true>(a[i], x);
                     const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[(n0 + i) * pitch + k0]);
 #pragma unroll
                     for (int k = 0; k < kSeg / 4; k++) {
@@ -181,9 +182,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
                     }
                 }
                 s.end[(turn * kMaxWarps + warp) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
-                // The same for all warps.  Decays of states that grow are left as their roots, as carried() takes them; for the
-                // others, where its product and comparison a state and segment cost 6 %, as they are.
-                const bool grows = !p.softplus || __any_sync(0xffffffffu, fmaxf(fmaxf(a2[0], a2[1]), fmaxf(a2[2], a2[3])) > 0.f);
+                // Decays of states that grow are left as their roots, as carried() takes them; for the others, where its product
+                // and comparison a state and segment cost 6 %, as they are.
+                const bool grows = warp_grows(p.softplus, a2);  // the same for all warps
                 const float fall_dt = grows ? 0.5f * sum_dt : sum_dt;
                 s.fall[(turn * kMaxWarps + warp) * 32 + lane] =
                     make_float4(decay(fall_dt * a2[0]), decay(fall_dt * a2[1]), decay(fall_dt * a2[2]), decay(fall_dt * a2[3]));
@@ -193,20 +194,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
                 h[1] = first.y;
                 h[2] = first.z;
                 h[3] = first.w;
-                for (int v = 0; v < warp + (ends ? 1 : 0); v++) {
-                    const float4 e = s.end[(turn * kMaxWarps + v) * 32 + lane], f = s.fall[(turn * kMaxWarps + v) * 32 + lane];
-                    if (grows) {
-                        h[0] = carried(h[0], f.x, f.x, e.x);
-                        h[1] = carried(h[1], f.y, f.y, e.y);
-                        h[2] = carried(h[2], f.z, f.z, e.z);
-                        h[3] = carried(h[3], f.w, f.w, e.w);
-                    } else {
-                        h[0] = fmaf(f.x, h[0], e.x);
-                        h[1] = fmaf(f.y, h[1], e.y);
-                        h[2] = fmaf(f.z, h[2], e.z);
-                        h[3] = fmaf(f.w, h[3], e.w);
+                const auto fold = [&](auto grow) {
+                    for (int v = 0; v < warp + (ends ? 1 : 0); v++) {
+                        const float4 e = s.end[(turn * kMaxWarps + v) * 32 + lane], f = s.fall[(turn * kMaxWarps + v) * 32 + lane];
+                        const float es[kStates] = {e.x, e.y, e.z, e.w}, fs[kStates] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int i = 0; i < kStates; i++) h[i] = decltype(grow)::value ? carried(h[i], fs[i], fs[i], es[i]) : fmaf(fs[i], h[i], es[i]);
                     }
-                }
+                };
+                grows ? fold(std::true_type{}) : fold(std::false_type{});
                 if (ends) {
                     if (warp == warps - 1) s.h[((buf ^ 1) * groups + g) * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
                     continue;

@@ -252,6 +252,16 @@ def test_growth_that_overflows_over_tokens_of_a_tiny_state(ttt, B, T, C, N, step
     check_forward(forward(ttt, bc.cuda(i), dt_softplus=False), i, softplus=False)
 
 
+@pytest.mark.parametrize("B,T,C,N", [(1, 8, 9, 16), (1, 60, 9, 16), (1, 700, 8, 5), (40, 60, 9, 16), (40, 60, 9, 20)])
+def test_growth_by_a_little_a_token(ttt, B, T, C, N):
+    """Growth just inside the decays near 1 (2^(1/16)), the same every token: an error of the decay would add up."""
+    i = growing(B, T, C, N, torch.full((T,), 0.043), state=1.0)
+    check_forward(forward(ttt, bc.cuda(i), dt_softplus=False), i, softplus=False)
+    dy = torch.zeros(B, T, C)
+    dy[:, -1] = 1.0
+    check_backward(backward(ttt, bc.cuda(i), dy.cuda(), dt_softplus=False), i, dy, None, softplus=False)
+
+
 def test_backward_of_growth_that_overflows_over_a_part(ttt):
     """The time axis in parts of 32 tokens: e^3 a token over the first 40, then a state that stays."""
     B, T, C, N = 1, 2048, 8, 4
