@@ -24,6 +24,12 @@ constexpr float kSmall = 0.0625f;
 constexpr float kQ0 = 0x1.62e42ep-1f, kQ1 = 0x1.ebf0e6p-3f, kQ2 = 0x1.bf5dd8p-5f;                              // x <= 0
 constexpr float kG0 = 0x1.62e430p-1f, kG1 = 0x1.ebfbe0p-3f, kG2 = 0x1.c6bb7ap-5f, kG3 = 0x1.3b2fc4p-7f;  // any x
 
+// A log2(e), infinity as the largest float: a step of zero, as padding has it, then still leaves the state as it is
+__device__ __forceinline__ float rate(float A) {
+    const float v = A * kLog2e;
+    return fabsf(v) == INFINITY ? copysignf(3.4028235e38f, v) : v;
+}
+
 __device__ __forceinline__ float decay(float x) {
     const float q = fmaf(fmaf(fmaf(kG3, x, kG2), x, kG1), x, kG0);
     const float near_one = fmaf(q, x, 1.f);

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(128) ttt_ssm_token_kernel(const Params p) {
     load_four<kVec>(p.A + (size_t)c * p.N + n0, live, a2);
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f, skip = on && p.D ? p.D[c] : 0.f;
 #pragma unroll
-    for (int i = 0; i < kStates; i++) a2[i] *= kLog2e;
+    for (int i = 0; i < kStates; i++) a2[i] = rate(a2[i]);
     for (int t = 0; t < p.T; t++) {
         const long long row = (long long)b * p.T + t;
         float Bt[kStates], Ct[kStates], dt = 0.f, u = 0.f, z = 0.f;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(128) ttt_ssm_token_kernel(const Params p) {
         for (int o = kLanes / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
         if (on && part == 0) {
             y = fmaf(skip, u, y);
-            const float out[1] = {p.z ? y * (z * sigmoid(z)) : y};
+            const float out[1] = {!token ? 0.f : p.z ? y * (z * sigmoid(z)) : y};
             store_vec<1>(static_cast<T*>(p.y) + row * p.C + c, out);
         }
     }

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
 #pragma unroll
     for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N;
-        a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
+        a2[i] = live ? rate(p.A[(size_t)c * p.N + n0 + i]) : 0.f;
         h[i] = !kEnds && live && p.h0 ? p.h0[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
         back[i] = 0.f;
         all[0][i] = all[1][i] = 1.f;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
 #pragma unroll
     for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N;
-        a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
+        a2[i] = live ? rate(p.A[(size_t)c * p.N + n0 + i]) : 0.f;
         g[i] = live && p.dh_T ? p.dh_T[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
         s.dA[i][tid] = 0.0;
     }

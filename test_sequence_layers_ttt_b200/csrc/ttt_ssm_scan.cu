@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(32 * (kWarps + kHelpers)) ttt_ssm_scan_kernel(
 #pragma unroll
     for (int i = 0; i < kStates; i++) {
         const bool live = on && n0 + i < p.N && warp < kWarps;
-        a2[i] = live ? p.A[(size_t)c * p.N + n0 + i] * kLog2e : 0.f;
+        a2[i] = live ? rate(p.A[(size_t)c * p.N + n0 + i]) : 0.f;
         h[i] = live && p.h0 ? p.h0[((size_t)b * p.C + c) * p.N + n0 + i] : 0.f;
     }
     // the recursion over tile m

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) ttt_ssm_segments_kernel(con
         for (int i = 0; i < kStates; i++) {
             const int n = (g * kQ + part) * kStates + i;
             h[i] = on && n < p.N && p.h0 && rank == 0 ? p.h0[((size_t)b * p.C + c) * p.N + n] : 0.f;
-            v[i] = on && n < p.N ? p.A[(size_t)c * p.N + n] * kLog2e : 0.f;
+            v[i] = on && n < p.N ? rate(p.A[(size_t)c * p.N + n]) : 0.f;
         }
         s.h[g * 32 + lane] = make_float4(h[0], h[1], h[2], h[3]);
         s.a2[g * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);

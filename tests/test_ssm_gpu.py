@@ -95,6 +95,27 @@ def test_padded_batch(ttt, B, T, C, N, kind):
     assert torch.equal(h[B // 2].cpu(), i["h0"][B // 2])  # the empty sequence's state
 
 
+# one sequence of a few tokens, of several tiles, in a cluster; many sequences, with few and many states
+@pytest.mark.parametrize("B,T,C,N", [(3, 8, 9, 16), (3, 70, 9, 16), (2, 1100, 8, 5), (40, 70, 33, 16), (40, 70, 9, 20)])
+def test_states_that_forget_at_once(ttt, B, T, C, N):
+    """A of minus infinity is the limit of large ones: padding and what fills up the last tile still leave the state."""
+    i = bc.cuda(bc.ssm_inputs(B, T, C, N, "f32", seed=30))
+    n = bc.lengths_for(B, T, torch.Generator().manual_seed(31)).cuda()
+    got = []
+    for large in (-float("inf"), -1e30):
+        i["A"][:, 0] = large
+        got.append([*forward(ttt, i, lengths=n), *backward(ttt, i, i["u"], i["h0"], lengths=n).values()])
+    for a, b in zip(*got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+def test_padding_has_zeros_behind_an_infinite_state(ttt):
+    i = bc.cuda(bc.ssm_inputs(2, 8, 9, 4, "f32", seed=32))
+    i["h0"][:, 3] = float("inf")
+    y, _ = forward(ttt, i, lengths=torch.tensor([5, 0], dtype=torch.int32, device="cuda"))
+    assert not y[0, 5:].any() and not y[1].any()
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("before,after", [(0, 64), (16, 16), (3, 2)])
 def test_slices_of_wider_rows(ttt, before, after, kind):
