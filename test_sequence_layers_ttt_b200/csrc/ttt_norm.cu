@@ -35,10 +35,17 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleMin = 7.888609052210118e-31f;  // 2^-100: a row of zeros has zeros and this scale
 
+// The larger one, NaN where either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Two values reduced over the row's threads at once: (sum, sum) or (sum, max).
 template <bool kMax>
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
-    return make_float2(a.x + b.x, kMax ? fmaxf(a.y, b.y) : a.y + b.y);
+    return make_float2(a.x + b.x, kMax ? max_nan(a.y, b.y) : a.y + b.y);
 }
 
 // blockDim.x threads a row: a power of two up to a warp, or whole warps.  `s` is free again after the next
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(512, sizeof(T) == 2 && kNV <= 2 ? 2 : 1) ttt_r
                 if constexpr (kQ8) {
                     float lo, hi;
                     unpack2(h[i][k], lo, hi);
-                    most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+                    most = max_nan(most, max_nan(fabsf(lo), fabsf(hi)));
                 }
             }
         }
@@ -175,8 +182,8 @@ __global__ void __launch_bounds__(512, sizeof(T) == 2 && kNV <= 2 ? 2 : 1) ttt_r
         if (kQ8) {
             float scale = acc.y * r / kE4m3Max;
             factor = kE4m3Max / acc.y;
-            if (r != r) {
-                scale = factor = r;
+            if (scale != scale) {  // of NaN in the row or the weight, or of infinity, whose r is zero
+                factor = scale;
             } else if (!(scale >= kScaleMin)) {
                 scale = kScaleMin;
                 factor = fminf(r * (1.f / kScaleMin), 3e38f);

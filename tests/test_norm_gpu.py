@@ -85,6 +85,21 @@ def test_nan_and_infinity_stay_in_their_row(ttt):
         assert torch.equal(y[0, row], clean[0, row]) and torch.isfinite(q[0, row].float()).all()
 
 
+@pytest.mark.parametrize("d", [40, 300, 2047, 2048, 9001])
+@pytest.mark.parametrize("weight", [1.0, float("nan"), float("inf"), 0.0])
+def test_q8_of_values_that_are_not_finite(ttt, d, weight):
+    """Scale and q are NaN, or finite, where the formula's are; an infinite weight makes an infinite scale."""
+    x, _, w = inputs(1, 6, d, "f32", False)
+    w[3] = weight
+    x[0, 1, 7], x[0, 2, d - 1], x[0, 3, 3], x[0, 4, 0] = float("nan"), float("inf"), -float("inf"), float("inf")
+    q, scale, _ = ttt.ttt_rmsnorm_q8_forward(x.cuda(), w.cuda())
+    (y, _), _ = ob.rmsnorm(x, w)
+    want = y.abs().amax(-1) / 448.0
+    q, scale = q.cpu().double(), scale.cpu().double()
+    assert torch.equal(torch.isnan(scale), torch.isnan(want)) and torch.equal(torch.isinf(scale), torch.isinf(want))
+    assert torch.equal(torch.isnan(q), torch.isnan(y / want[..., None]))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("past", [True, False])
 @pytest.mark.parametrize("B,T,d", [(1, 1, 1), (2, 3, 7), (1, 5, 32), (3, 50, 100), (2, 9, 256), (2, 200, 768),
