@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwd
         unpack2(dot, b0, b1);
         const float2 acc = reduce_row<false>(make_float2(a0 + a1, b0 + b1), s[buf]);
         const float r = rsqrtf(acc.x / (float)p.d + p.eps);
-        const float c = -r * r * r * (acc.y / (float)p.d);
+        const float c = -(acc.y / (float)p.d * r) * r * r;  // in this order: r^3 alone passes the floats' range for tiny and for large rows
         const f2 r2 = pack2(r, r), c2 = pack2(c, c);
         T* out = static_cast<T*>(p.dh) + (size_t)row * p.d;
         if (kPastLate) fetch_past();

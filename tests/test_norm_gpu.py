@@ -115,6 +115,20 @@ def test_backward(ttt, B, T, d, past, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [100, 2048, 9001])
+def test_backward_of_tiny_and_large_rows(ttt, d, kind):
+    """Rows of zeros, of 1e-14 and of 1e14 and 1e17, whose inverse norm's third power is no float."""
+    x, r, w = inputs(1, 5, d, kind, True, seed=4)
+    x = (x.float() * torch.tensor([0.0, 1e-14, 1.0, 1e14, 1e17])[None, :, None]).to(x.dtype)
+    dy = bc.normal(torch.Generator().manual_seed(11), 1, 5, d).to(x.dtype)
+    for past in (None, r):
+        dh, dw = ttt.ttt_rmsnorm_backward(x.cuda(), w.cuda(), dy.cuda(), up(past), eps=1e-30)
+        (dho, dhe), (dwo, dwe) = ob.rmsnorm_backward(x, w, dy, past, eps=float(torch.tensor(1e-30)))
+        bc.close("dh", dh, dho, dhe)
+        bc.close("dweight", dw, dwo, dwe)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,d", [(64, 300, 5), (8, 1000, 64), (3, 2000, 96), (1, 4000, 200), (1, 400, 9001),
                                    (2, 170, 11000), (1, 300, 13004), (1, 310, 16383)])
 def test_many_rows(ttt, B, T, d, kind):
