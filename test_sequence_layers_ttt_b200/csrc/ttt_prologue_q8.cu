@@ -143,7 +143,8 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         ptx::fence_mbar_init();
     }
     if (warp == 1) tc05::tmem_alloc(ptx::smem_addr(&s.tmem_base), kTmemCols);
-    if (tid < kD / 2) s.turn[tid] = (unsigned long long)(exp2(64.0 - (2.0 * tid / kD) * log2((double)p.rope_base)) * 0.15915494309189535);
+    if (tid < kD / 2)  // the constant is 2^64 / (2 pi); 64 in the exponent would cost the double four bits
+        s.turn[tid] = (unsigned long long)(exp2(-(2.0 * tid / kD) * log2((double)p.rope_base)) * 2935890503282001226.0);
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
@@ -263,8 +264,9 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                 const bool rope = p.rotary && proj < 2;
                 // the rotation of this token row, shared by the tile's four heads, times the token's scale: angle
                 // pos * base^(-2i/d) in fixed point, whose overflow leaves whole turns out, then sin and cos by the
-                // special-function unit: the angle is off by 4e-7 and they by 5e-7 at most, against the outputs'
-                // half step of 2^-8.  (In double the reduction took as long as both functions.)
+                // special-function unit: the angle is off by half of 2^-23 turns, 3.7e-7, and by the step's rounding,
+                // pos 2^-54 turns (2e-11 at position 50000, 7e-7 near 2^31), and they by 5e-7 at most, against the
+                // outputs' half step of 2^-8.  (In double the reduction took as long as both functions.)
                 f2 cs[16], sn[16];  // of two neighbouring features each
                 if (rope) {
                     const unsigned long long pos = (unsigned long long)((long long)p.pos0 + t);
@@ -273,8 +275,9 @@ ttt_prologue_q8_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                         float c[2], n[2];
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
-                            // the fraction of a turn, exact to 2^-46; its top 23 bits become a float in [-1/2, 1/2)
-                            const uint32_t phase = (uint32_t)((pos * s.turn[2 * i + k]) >> 32) + 0x80000000u;
+                            // the fraction of a turn to the nearest 2^-23, a float in [-1/2, 1/2); what passes 1/2 comes
+                            // back at -1/2, the same angle
+                            const uint32_t phase = (uint32_t)((pos * s.turn[2 * i + k]) >> 32) + 0x80000100u;
                             const float r = (__uint_as_float(0x3f800000u | (phase >> 9)) - 1.5f) * 6.283185307179586f;
                             c[k] = sx * __cosf(r);
                             n[k] = sx * __sinf(r);

@@ -65,6 +65,43 @@ def test_against_the_oracle(ttt, B, T, H, dm, pos0, rotary):
     compare(out, oracle(ops, pos0=pos0, rotary=rotary, eta_base=0.5))
 
 
+def angles(ttt, pos0, T):
+    """How far the rotation's angles are off, at the positions and features whose sine is near zero, where bf16 resolves it:
+    Q is -sin in its first 32 features and cos in the others.  Returns (sines near zero, errors of their angles)."""
+    H, dm = 4, 16
+    x = torch.zeros(1, T, dm)
+    x[..., 0] = 1.0
+    theta = torch.zeros(H, 64, dm)
+    theta[:, 32:, 0] = 1.0
+    f8, one = theta.to(torch.float8_e4m3fn).cuda(), torch.ones(H, 64, device="cuda")
+    lr = torch.zeros(H, dm, device="cuda").to(torch.float8_e4m3fn)
+    Q = ttt.ttt_prologue_q8_forward(x.to(torch.float8_e4m3fn).cuda(), torch.ones(1, T, device="cuda"), f8, one, f8, one, f8, one,
+                                    lr, one[:, 0].contiguous(), one[:, 0].contiguous(), pos0=pos0)[0]
+    got = -Q[0, 0, :, :32].float().cpu().numpy().astype(np.float64)
+    wide = np.longdouble  # 64 bits of mantissa
+    pos = np.arange(pos0, pos0 + T).astype(wide)[:, None]
+    angle = pos * wide(10000) ** (-np.arange(32).astype(wide) / 32)
+    turns = angle / (2 * np.arccos(wide(-1)))
+    r = ((turns - np.rint(turns)) * (2 * np.arccos(wide(-1)))).astype(np.float64)
+    return np.sin(r), got - np.sin(r), np.cos(r)
+
+
+def test_rotary_angles_are_rounded_to_both_sides(ttt):
+    """Angles in steps of 2^-23 turns (7.5e-7): their errors, 2.2e-7 in the mean square, average out.  With sines below 5e-4
+    the outputs' rounding is as small, and the mean of 300 such errors stays below 1.5e-7, five of its deviations and more."""
+    s, e, c = angles(ttt, 0, 65536)
+    near = (np.abs(s) < 5e-4) & (c > 0)
+    assert near.sum() > 300 and abs(e[near].mean()) <= 1.5e-7
+
+
+def test_rotary_angles_at_far_positions(ttt):
+    """Near 2^31: half a step of 2^-23 turns, 3.75e-7; a rounding and a half of a double at that position, 7.2e-7; the sine's
+    documented 2^-21.4; and half a step of the output at 5e-5."""
+    s, e, _ = angles(ttt, 2 ** 31 - 2 ** 18, 2 ** 18)
+    near = np.abs(s) < 5e-5
+    assert near.sum() > 100 and np.abs(e[near]).max() <= 3.75e-7 + 7.2e-7 + 2 ** -21.4 + 2.0 ** -9 * 5e-5
+
+
 def test_many_heads(ttt):
     """H = 256: the learning-rate tile is as wide as the others."""
     ops = make(ttt, 1, 40, 256, 64, 1)
