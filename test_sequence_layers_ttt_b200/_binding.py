@@ -576,10 +576,17 @@ def _workspace(given: Optional[torch.Tensor], need: int, like: torch.Tensor):
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
+def _sizes(t: torch.Tensor, name: str):
+    """The shape, whose sizes the library takes as C ints: ctypes would drop what passes them without a word."""
+    if max(t.shape) > 0x7fffffff:
+        raise ValueError(f"{name} has a size past 2^31 - 1: {list(t.shape)}")
+    return t.shape
+
+
 def _three(t: torch.Tensor, name: str):
     if t.dim() != 3 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor [B, T, width]")
-    return t.shape
+    return _sizes(t, name)
 
 
 def ttt_rmsnorm_forward(x, weight, residual=None, *, eps: float = 1e-6, y=None, h=None, stream=None):
@@ -650,7 +657,10 @@ def ttt_prologue_q8_forward(x, scale_x, theta_q, scale_q, theta_k, scale_k, thet
     B, T, dm = _three(x, "x")
     if theta_q.dim() != 3:
         raise ValueError("theta_q must be [H, d, d_model]")
-    H, d = theta_q.shape[:2]
+    H, d, _ = _sizes(theta_q, "theta_q")
+    pos0 = int(pos0)
+    if not -2 ** 31 <= pos0 < 2 ** 31:
+        raise ValueError(f"pos0 must lie within 32 bits, got {pos0}")
     dev, f8, f32 = x.device, torch.float8_e4m3fn, torch.float32
     ptrs = [_dense(x, "x", (B, T, dm), f8, dev), _dense(scale_x, "scale_x", (B, T), f32, dev)]
     for name, w, sc in (("q", theta_q, scale_q), ("k", theta_k, scale_k), ("v", theta_v, scale_v)):
@@ -665,7 +675,7 @@ def ttt_prologue_q8_forward(x, scale_x, theta_q, scale_q, theta_k, scale_k, thet
         for name, o in (("Q", Q), ("K", K), ("V", V)):
             ptrs.append(_dense(o, name, (B, H, T, d), torch.bfloat16, dev))
         ptrs.append(_dense(eta, "eta", (B, H, T), f32, dev))
-        _check(lib.ttt_prologue_q8_forward(B, T, H, d, dm, int(pos0), float(eta_base), float(rope_base),
+        _check(lib.ttt_prologue_q8_forward(B, T, H, d, dm, pos0, float(eta_base), float(rope_base),
                                            int(bool(rotary)), *ptrs, s))
     return Q, K, V, eta
 
@@ -680,7 +690,7 @@ def _conv_args(x, weight, bias, state, lengths, state_name="state0"):
     B, T, C = _three(x, "x")
     if weight.dim() != 2:
         raise ValueError("weight must be [C, width]")
-    W = weight.shape[1]
+    W = _sizes(weight, "weight")[1]
     dev, dt = x.device, x.dtype
     code = _token_dtype(x, "x")
     px, ld = _rows(x, "x", (B, T, C), dt, dev)
@@ -743,7 +753,7 @@ def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, h0, lengths, h_name="h0"):
     B, T, C = _three(u, "u")
     if A.dim() != 2:
         raise ValueError("A must be [C, N]")
-    N = A.shape[1]
+    N = _sizes(A, "A")[1]
     dev, ty, f32 = u.device, u.dtype, torch.float32
     code = _token_dtype(u, "u")
     pu, lu = _rows(u, "u", (B, T, C), ty, dev)

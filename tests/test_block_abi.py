@@ -163,6 +163,31 @@ def test_binding_names_the_argument():
         b._silu_code("relu")
 
 
+def test_binding_refuses_sizes_past_31_bits():
+    """Sizes that ctypes would cut to the library's 32 bits: the call would work on the first few tokens alone."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    far = 2 ** 32 + 8
+    with FakeTensorMode():
+        cuda = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="cuda:0")
+        f32, f8 = torch.float32, torch.float8_e4m3fn
+        x = cuda(1, far, 1)
+        w, A = cuda(1, dtype=f32), cuda(1, far, dtype=f32)
+        pro = [cuda(1, 4, 16, dtype=f8), cuda(1, 4, dtype=f32)] + [cuda(4, 64, 16, dtype=f8), cuda(4, 64, dtype=f32)] * 3 + [
+            cuda(4, 16, dtype=f8), cuda(4, dtype=f32), cuda(4, dtype=f32)]
+        u, B = cuda(1, 1, 1), cuda(1, 1, far)
+        for call in (lambda: b.ttt_rmsnorm_forward(x, w), lambda: b.ttt_rmsnorm_q8_forward(x, w),
+                     lambda: b.ttt_rmsnorm_backward(x, w, x), lambda: b.ttt_conv_forward(x, cuda(1, 4, dtype=f32)),
+                     lambda: b.ttt_conv_backward(x, cuda(1, 4, dtype=f32), None, x),
+                     lambda: b.ttt_conv_decode(u, cuda(1, far, dtype=f32), None, cuda(1, far - 1, 1)),
+                     lambda: b.ttt_ssm_forward(x, x, cuda(1, 1, dtype=f32), x, x),
+                     lambda: b.ttt_ssm_forward(u, u, A, B, B), lambda: b.ttt_ssm_backward(u, u, A, B, B, u),
+                     lambda: b.ttt_ssm_decode(u, u, A, B, B, cuda(1, 1, far, dtype=f32))):
+            with pytest.raises(ValueError, match="past 2\\^31"):
+                call()
+        with pytest.raises(ValueError, match="pos0"):
+            b.ttt_prologue_q8_forward(*pro, pos0=2 ** 31)
+
+
 def test_q8_weights_layout():
     g = torch.Generator().manual_seed(0)
     theta = torch.randn(3, 32, 64, generator=g)
