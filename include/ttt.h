@@ -419,6 +419,7 @@ ttt_status ttt_rmsnorm_backward(int B, int T, int d, ttt_dtype dtype, float eps,
  *   theta_lr [H][d_model] e4m3;  scale_lr [H] fp32;  b_lr [H] fp32
  * Built for d = 64, d_model a multiple of 16, H a multiple of 4 up to 256
  * (TTT_ERR_UNSUPPORTED otherwise); T >= 1.
+ * rope_base is finite and above 1 (TTT_ERR_SHAPE).
  */
 ttt_status ttt_prologue_q8_forward(int B, int T, int H, int d, int d_model, int pos0, float eta_base,
                                    float rope_base, int rotary, const void* x, const float* scale_x,

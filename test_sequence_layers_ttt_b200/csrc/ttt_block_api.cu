@@ -1,5 +1,6 @@
 // Host layer of the operators around the sequence layer (include/ttt.h, second half): argument checks
 // and launches.  Checks run on the host alone; a call that fails one launches nothing.
+#include <cfloat>
 #include <climits>
 
 #include "api_util.h"
@@ -87,7 +88,7 @@ ttt_status check_norm_backward(const NormBwdArgs& a, const void* workspace, size
 // ---------------------------------------------------------------- 8-bit prologue
 ttt_status check_prologue_q8(const PrologueArgs& a, const PrologueScales& s) {
     if (a.B < 1 || a.T < 1 || a.H < 1 || a.d_model < 1 || !tokens_fit(a.B, a.T)) return TTT_ERR_SHAPE;
-    if (!(a.rope_base > 1.f) || !(a.eta_base == a.eta_base)) return TTT_ERR_SHAPE;
+    if (!(a.rope_base > 1.f && a.rope_base <= FLT_MAX) || !(a.eta_base == a.eta_base)) return TTT_ERR_SHAPE;
     if (!prologue_q8_supports(a.B, a.T, a.H, a.d, a.d_model)) return TTT_ERR_UNSUPPORTED;
     const void* const req[] = {a.x, s.x, a.theta_q, s.q, a.theta_k, s.k, a.theta_v, s.v, a.theta_lr, s.lr,
                                a.b_lr, a.Q, a.K, a.V, a.eta};

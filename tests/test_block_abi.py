@@ -70,6 +70,11 @@ def test_prologue_q8_refusals(kw, code):
     assert pro(**kw) == code
 
 
+def test_prologue_q8_refuses_an_infinite_rope_base():
+    """Its first feature's step would be 0 times infinity."""
+    assert pro(base=float("inf")) == SHAPE and pro(base=float("nan")) == SHAPE
+
+
 # ---------------------------------------------------------------- convolution
 def conv(B=2, T=5, C=8, W=4, dtype=0, ld=8, **at):  # x weight bias state0 lengths y state_T
     return b.lib.ttt_conv_forward(B, T, C, W, dtype, 1, ld, *fake(7, **at), None)
