@@ -9,6 +9,8 @@ import torch
 import torch.nn.functional as F
 
 import block_cases as bc
+import oracle
+from oracle import prologue as oracle_prologue
 
 pytestmark = pytest.mark.gpu
 
@@ -170,6 +172,35 @@ def test_the_ttt_layer_from_8_bits(ttt):
     assert torch.isfinite(Z).all() and torch.isfinite(W_T).all()
     again = ttt.ttt_linear_forward(Q, K, V, eta, W0, b0, gam, bet)
     assert torch.equal(Z, again[0])
+
+
+def test_the_ttt_layer_from_8_bits_against_the_oracles(ttt):
+    """The same chain, each link against its float64 oracle on the values that the link before has left: 8 bits to Q, K, V
+    within half a bf16 step and the 1e-5 of the prologue's own test, and those to the scan's outputs at its bar for bf16
+    inputs, 3e-3 of the RMS."""
+    B, T, H, dm = 2, 75, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rnd = lambda *s, std=1.0: torch.randn(s, generator=g, device="cuda") * std
+    x, res = rnd(B, T, dm).bfloat16(), rnd(B, T, dm).bfloat16()
+    q, scale, _ = ttt.ttt_rmsnorm_q8_forward(x, 1 + rnd(dm, std=0.1), res)
+    ws = [ttt.prologue_q8_weights(rnd(H, dm, 64, std=dm ** -0.5)) for _ in range(3)] + [
+        ttt.prologue_q8_weights(rnd(H, dm, std=dm ** -0.5))]
+    b = rnd(H)
+    out = ttt.ttt_prologue_q8_forward(q, scale, *(t for w in ws for t in w), b, pos0=9)
+    wide = [(w.cpu().double() * s.cpu().double()[..., None]) for w, s in ws]
+    ref = oracle_prologue.project((q.cpu().double() * scale.cpu().double()[..., None]), *(t.transpose(1, 2) for t in wide[:3]), wide[3],
+                                  b.cpu(), pos0=9)
+    for got, want in zip(out[:3], ref[:3]):
+        got, want = got.cpu().double(), torch.as_tensor(want)
+        assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5 * want.square().mean().sqrt()).all()
+    eta = torch.as_tensor(ref[3])
+    assert ((out[3].cpu().double() - eta).abs() <= 2e-5 * eta).all()
+    W0, b0 = rnd(B, H, 64, 64, std=0.02), rnd(B, H, 64, std=0.02)
+    gam, bet = 1 + rnd(H, 64, std=0.1), rnd(H, 64, std=0.1)
+    scan = ttt.ttt_linear_forward(*out, W0, b0, gam, bet)
+    for got, want in zip(scan, oracle.ttt_linear(*(t.cpu().double().numpy() for t in (*out, W0, b0, gam, bet)), 16)):
+        want = torch.as_tensor(want)
+        assert (got.cpu().double() - want).abs().max() <= 3e-3 * want.square().mean().sqrt()
 
 
 def every_call(ttt, i, x, w, cw, q8):

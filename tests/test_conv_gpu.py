@@ -174,6 +174,19 @@ def test_offsets_past_32_bits(ttt):
     assert torch.equal(y[-1:], y1) and torch.equal(st[-1:], st1)
 
 
+def test_gradient_offsets_past_32_bits(ttt):
+    """2.2e9 elements, all but the last sequence zeros: its gradients equal those of itself alone."""
+    B, T, C = 33, 8192, 8192
+    x = torch.zeros(B, T, C, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x[-1] = torch.randn(T, C, generator=g, device="cuda").bfloat16()
+    w = torch.randn(C, 4, generator=g, device="cuda")
+    dx, dw, _, _ = ttt.ttt_conv_backward(x, w, None, x)
+    one, dw1, _, _ = ttt.ttt_conv_backward(x[-1:].contiguous(), w, None, x[-1:].contiguous())
+    assert torch.equal(dx[-1:], one) and not dx[0].any()
+    assert torch.allclose(dw, dw1, rtol=1e-4, atol=1e-4 * float(dw1.abs().max()))  # 8192 terms, other pieces of the tokens
+
+
 def test_refusals_of_the_binding(ttt):
     x, w, b, s, g = inputs(2, 6, 16, 4, "f32")
     x, w, s = x.cuda(), w.cuda(), s.cuda()

@@ -145,6 +145,24 @@ def test_many_rows(ttt, B, T, d, kind):
     bc.close("dweight", dw, dwo, dwe)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("B,T,d", [(64, 300, 5), (8, 1000, 64), (3, 2000, 96), (1, 4000, 200), (1, 400, 9001),
+                                   (2, 170, 11000), (1, 300, 13004), (1, 310, 16383), (1, 310, 16384)])
+def test_q8_of_many_rows(ttt, B, T, d, residual, kind):
+    """More rows than the blocks take at once, and rows that take most of an SM's registers."""
+    x, r, w = inputs(B, T, d, kind, residual, seed=5)
+    q, scale, h = ttt.ttt_rmsnorm_q8_forward(x.cuda(), w.cuda(), up(r))
+    (yo, ye), (ho, he) = ob.rmsnorm(x, w, r)
+    if residual:
+        bc.close("h", h, ho, he)
+    so = yo.abs().amax(-1) / 448.0
+    bc.close("scale", scale, so, ye.amax(-1) / 448.0 + 4 * ob.U * so)
+    v, s = q.cpu().double(), scale.cpu().double()[..., None]
+    bound = s * (yo.abs() / s * 2.0 ** -4 + 2.0 ** -10) + 2 * ye + 4 * ob.U * yo.abs()
+    assert float(v.abs().amax(-1).min()) == 448.0 and ((v * s - yo).abs() <= bound).all()
+
+
 def test_backward_twice_is_the_same(ttt):
     x, r, w = (t.cuda() for t in inputs(4, 999, 512, "bf16", True))
     one, two = (ttt.ttt_rmsnorm_backward(x, w, r) for _ in range(2))
@@ -168,6 +186,19 @@ def test_offsets_past_32_bits(ttt):
     y, _ = ttt.ttt_rmsnorm_forward(x, w)
     alone, _ = ttt.ttt_rmsnorm_forward(x[:, -7:].contiguous(), w)
     assert torch.equal(y[:, -7:], alone)
+
+
+def test_gradient_offsets_past_32_bits(ttt):
+    """2.2e9 elements, all but the last rows zeros: their gradients equal those of these rows on their own."""
+    rows, d = 1_080_000, 2048
+    x = torch.zeros(1, rows, d, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x[0, -7:] = torch.randn(7, d, generator=g, device="cuda").bfloat16()
+    w = torch.rand(d, generator=g, device="cuda")
+    dh, dw = ttt.ttt_rmsnorm_backward(x, w, x, x)
+    one, dw1 = ttt.ttt_rmsnorm_backward(*(t[:, -7:].contiguous() if t is x else t for t in (x, w, x, x)))
+    assert torch.equal(dh[:, -7:], one) and not dh[0, :1000].any()
+    assert torch.allclose(dw, dw1, rtol=1e-5, atol=1e-5 * float(dw1.abs().max()))
 
 
 def test_refusals_of_the_binding(ttt):

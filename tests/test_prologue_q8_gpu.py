@@ -102,6 +102,13 @@ def test_rotary_angles_at_far_positions(ttt):
     assert near.sum() > 100 and np.abs(e[near]).max() <= 3.75e-7 + 7.2e-7 + 2 ** -21.4 + 2.0 ** -9 * 5e-5
 
 
+@pytest.mark.parametrize("B,T", [(64, 1), (150, 1), (50, 3), (5, 33)])
+def test_streams_that_end_within_a_warp(ttt, B, T):
+    """One token, or a few, of many streams: a tile's rows belong to as many sequences."""
+    ops = make(ttt, B, T, 8, 144, B)
+    compare(ttt.ttt_prologue_q8_forward(*(t.cuda() for t in ops), pos0=1971), oracle(ops, pos0=1971))
+
+
 def test_many_heads(ttt):
     """H = 256: the learning-rate tile is as wide as the others."""
     ops = make(ttt, 1, 40, 256, 64, 1)

@@ -232,6 +232,21 @@ def test_few_tokens_and_many_rows(ttt, B, T, C, N, kind):
     check_forward(forward(ttt, bc.cuda(i), lengths=n.cuda()), i, lengths=n)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,C,N", [(20, 300, 64, 64), (38, 300, 32, 33), (70, 290, 20, 20)])
+def test_more_than_16_states_in_parts(ttt, B, T, C, N, kind):
+    """32 channels a block and the tokens shared out in clusters of two or four blocks: padded, with the state in place."""
+    i = bc.ssm_inputs(B, T, C, N, kind, seed=33)
+    n = bc.lengths_for(B, T, torch.Generator().manual_seed(34))
+    for b in range(B):
+        for k in ("u", "dt", "Bm", "Cm", "z"):
+            i[k][b, n[b]:] = NAN
+    c = bc.cuda(i)
+    y, h = forward(ttt, c, h_T=c["h0"], lengths=n.cuda())
+    assert h is c["h0"]
+    check_forward((y, h), i, lengths=n)
+
+
 def test_few_rows_in_parts_of_growing_states(ttt):
     i = bc.ssm_inputs(1, 600, 20, 8, "f32", seed=24, softplus=False)
     i["A"] = -0.02 * i["A"]
@@ -400,6 +415,26 @@ def test_offsets_past_32_bits(ttt):
     del u, dt
     ya, ha = forward(ttt, last)
     assert torch.allclose(y[-1:].float(), ya.float(), rtol=2 ** -7, atol=1e-5) and torch.allclose(h[-1:], ha, rtol=1e-4, atol=1e-6)
+
+
+def test_gradient_offsets_past_32_bits(ttt):
+    """2.2e9 elements, all but the last sequence zeros: its gradients equal those of itself alone."""
+    B, T, C, N = 66, 4096, 8192, 2
+    g = torch.Generator(device="cuda").manual_seed(0)
+    u = torch.zeros(B, T, C, dtype=torch.bfloat16, device="cuda")
+    u[-1] = torch.randn(T, C, generator=g, device="cuda").bfloat16()
+    dt = torch.full_like(u, -2.0)
+    Bm = torch.randn(B, T, N, generator=g, device="cuda").bfloat16()
+    A = -torch.ones(C, N, device="cuda")
+    alone = backward(ttt, {"u": u[-1:].contiguous(), "dt": dt[-1:].contiguous(), "A": A, "Bm": Bm[-1:].contiguous(),
+                           "Cm": Bm[-1:].contiguous()}, u[-1:].contiguous())
+    whole = backward(ttt, {"u": u, "dt": dt, "A": A, "Bm": Bm, "Cm": Bm}, u)
+    for k, v in alone.items():
+        if v is not None:
+            got = whole[k] if k == "dA" else whole[k][-1:]
+            # rows are rounded to bf16 once each; sums go by other parts of the time axis
+            assert torch.allclose(got.float(), v.float(), rtol=2 ** -7, atol=1e-4 * float(v.float().abs().max())), k
+            assert k == "dA" or not whole[k][0].any(), k
 
 
 def test_refusals_of_the_binding(ttt):
