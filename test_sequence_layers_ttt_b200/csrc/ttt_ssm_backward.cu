@@ -25,6 +25,7 @@
 #include "ssm_params.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace ttt {
 namespace {
@@ -71,7 +72,7 @@ __device__ __forceinline__ size_t carry_at(const SsmBwdParams& p, int b, int seg
 }
 // v folded over `count` parts from part `from` on, in steps of `by`; m as in carry_at.  Eight parts' values are on
 // their way at a time (four where a thread has 128 registers): one by one, 64 parts took longer than a walk along one of them.
-template <int kNp>
+template <int kNp, bool kGrow>
 __device__ __forceinline__ void fold(float (&v)[kStates], const SsmBwdParams& p, int b, int from, int by, int count, int m,
                                      int n0, int c) {
     constexpr int kBatch = kNp > 16 ? 4 : 8;
@@ -82,18 +83,18 @@ __device__ __forceinline__ void fold(float (&v)[kStates], const SsmBwdParams& p,
             const bool live = j0 + j < count;
             const int seg = live ? from + (j0 + j) * by : 0;
             const float *pe = p.carry + carry_at<kNp>(p, b, seg, m, n0, c), *p0 = p.carry + carry_at<kNp>(p, b, seg, 2, n0, c);
-            const float* p1 = p.carry + carry_at<kNp>(p, b, seg, 3, n0, c);
+            const float* p1 = p.carry + carry_at<kNp>(p, b, seg, 3, n0, c);  // 1 where no state of the warp grows
 #pragma unroll
             for (int i = 0; i < kStates; i++) {
                 e[j][i] = live ? pe[(size_t)i * p.C] : 0.f;
                 a0[j][i] = live ? p0[(size_t)i * p.C] : 1.f;
-                a1[j][i] = live ? p1[(size_t)i * p.C] : 1.f;
+                a1[j][i] = kGrow && live ? p1[(size_t)i * p.C] : 1.f;
             }
         }
 #pragma unroll
         for (int j = 0; j < kBatch; j++)
 #pragma unroll
-            for (int i = 0; i < kStates; i++) v[i] = carried(v[i], a0[j][i], a1[j][i], e[j][i]);
+            for (int i = 0; i < kStates; i++) v[i] = kGrow ? carried(v[i], a0[j][i], a1[j][i], e[j][i]) : fmaf(a0[j][i], v[i], e[j][i]);
     }
 }
 
@@ -114,7 +115,8 @@ struct CkptSmem {
 
 // kK: tokens of a chunk; a tile is two chunks.  kEnds: a part of the time axis for itself, as carry has it.
 // The gradient that leaves a part to the one before is sum_t (a_first ... a_t) C_t dy'_t, so it too is
-// summed walking forwards; the product of the even tokens' decays and that of the odd ones' are kept apart, as carried() takes them.
+// summed walking forwards; of states that grow the product of the even tokens' decays and that of the odd ones' are kept
+// apart, as carried() takes them.
 template <typename T, int kNW, int kK, bool kEnds>
 __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmBwdParams p) {
     constexpr int kNp = kStates * kNW, kTile = 2 * kK, kThreads = 32 * kNW;
@@ -136,7 +138,13 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
         back[i] = 0.f;
         all[0][i] = all[1][i] = 1.f;
     }
-    if (!kEnds && on) fold<kNp>(h, p, w.b, 0, 1, w.seg, 0, n0, c);
+    const bool grows = warp_grows(p.softplus, a2);
+    if (!kEnds && on) {
+        if (grows)
+            fold<kNp, true>(h, p, w.b, 0, 1, w.seg, 0, n0, c);
+        else
+            fold<kNp, false>(h, p, w.b, 0, 1, w.seg, 0, n0, c);
+    }
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f;
     const long long row0 = (long long)w.b * p.T + w.t0;
     const auto stage = [&](int m) {
@@ -211,38 +219,46 @@ __global__ void __launch_bounds__(32 * kNW) ttt_ssm_checkpoint_kernel(const SsmB
                     dy[2 * q + 1] = f.y;
                 }
             }
+            const auto walk = [&](auto grow) {
 #pragma unroll
-            for (int i = 0; i < kStates; i++) {
-                const f2 A2 = pack2(a2[i], a2[i]);
-                f2 x[2 * kQ];
-                float a[4 * kQ];
+                for (int i = 0; i < kStates; i++) {
+                    const f2 A2 = pack2(a2[i], a2[i]);
+                    f2 x[2 * kQ];
+                    float a[4 * kQ];
 #pragma unroll
-                for (int k = 0; k < 2 * kQ; k++) x[k] = mul2(dt[k], A2);
-                decays<true>(a, x);
-                const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][half * kK]);
+                    for (int k = 0; k < 2 * kQ; k++) x[k] = mul2(dt[k], A2);
+                    decays<decltype(grow)::value>(a, x);
+                    const ulonglong2* Bi = reinterpret_cast<const ulonglong2*>(&s.b[n0 + i][half * kK]);
 #pragma unroll
-                for (int q = 0; q < kQ; q++) {
-                    const ulonglong2 Bq = Bi[q];
-                    float v0, v1, v2, v3;
-                    unpack2(mul2(du[2 * q], Bq.x), v0, v1);
-                    unpack2(mul2(du[2 * q + 1], Bq.y), v2, v3);
-                    h[i] = fmaf(a[4 * q], h[i], v0);
-                    h[i] = fmaf(a[4 * q + 1], h[i], v1);
-                    h[i] = fmaf(a[4 * q + 2], h[i], v2);
-                    h[i] = fmaf(a[4 * q + 3], h[i], v3);
-                    if constexpr (kEnds) {
-                        const ulonglong2 Cq = reinterpret_cast<const ulonglong2*>(&s.c[n0 + i][half * kK])[q];
-                        float g[4];
-                        unpack2(mul2(dy[2 * q], Cq.x), g[0], g[1]);
-                        unpack2(mul2(dy[2 * q + 1], Cq.y), g[2], g[3]);
+                    for (int q = 0; q < kQ; q++) {
+                        const ulonglong2 Bq = Bi[q];
+                        float v0, v1, v2, v3;
+                        unpack2(mul2(du[2 * q], Bq.x), v0, v1);
+                        unpack2(mul2(du[2 * q + 1], Bq.y), v2, v3);
+                        h[i] = fmaf(a[4 * q], h[i], v0);
+                        h[i] = fmaf(a[4 * q + 1], h[i], v1);
+                        h[i] = fmaf(a[4 * q + 2], h[i], v2);
+                        h[i] = fmaf(a[4 * q + 3], h[i], v3);
+                        if constexpr (kEnds) {
+                            const ulonglong2 Cq = reinterpret_cast<const ulonglong2*>(&s.c[n0 + i][half * kK])[q];
+                            float g[4];
+                            unpack2(mul2(dy[2 * q], Cq.x), g[0], g[1]);
+                            unpack2(mul2(dy[2 * q + 1], Cq.y), g[2], g[3]);
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            all[k & 1][i] *= a[4 * q + k];
-                            back[i] = carried(g[k], all[0][i], all[1][i], back[i]);
+                            for (int k = 0; k < 4; k++) {
+                                if constexpr (decltype(grow)::value) {
+                                    all[k & 1][i] *= a[4 * q + k];
+                                    back[i] = carried(g[k], all[0][i], all[1][i], back[i]);
+                                } else {
+                                    all[0][i] *= a[4 * q + k];
+                                    back[i] = fmaf(all[0][i], g[k], back[i]);
+                                }
+                            }
                         }
                     }
                 }
-            }
+            };
+            grows ? walk(std::true_type{}) : walk(std::false_type{});
         }
     }
     if (kEnds && on) {
@@ -310,7 +326,11 @@ __global__ void __launch_bounds__(32 * kNW, blocks_for(kNW)) ttt_ssm_backward_ke
         g[i] = live && p.dh_T ? p.dh_T[((size_t)w.b * p.C + c) * p.N + n0 + i] : 0.f;
         s.dA[i][tid] = 0.0;
     }
-    if (on) fold<kNp>(g, p, w.b, p.segs - 1, -1, p.segs - 1 - w.seg, 1, n0, c);
+    if (warp_grows(p.softplus, a2)) {
+        if (on) fold<kNp, true>(g, p, w.b, p.segs - 1, -1, p.segs - 1 - w.seg, 1, n0, c);
+    } else if (on) {
+        fold<kNp, false>(g, p, w.b, p.segs - 1, -1, p.segs - 1 - w.seg, 1, n0, c);
+    }
     const float bias = on && p.dt_bias ? p.dt_bias[c] : 0.f, skip = on && p.D ? p.D[c] : 0.f;
     double dD = 0.0, dbias = 0.0;
 
