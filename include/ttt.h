@@ -375,6 +375,8 @@ ttt_status ttt_linear_backward_static(int B, int H, int T, int d, int mini_batch
  * Root-mean-square norm with the residual's addition:
  *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight
  * over the d features of a token.  1 <= d <= 16384; B, T >= 1; eps > 0.
+ * A row whose squares add up past the largest float (|h| around 1e18) has y = 0;
+ * NaN and infinity reach their own row alone.
  *   x, residual  [B][T][d]; residual may be NULL (h = x)
  *   weight       [d] fp32
  *   y            [B][T][d]
@@ -389,6 +391,7 @@ ttt_status ttt_rmsnorm_forward(int B, int T, int d, ttt_dtype dtype, float eps, 
 /* The same norm with its output in 8 bits (e4m3) and a scale a token, as
  * ttt_prologue_q8_forward reads them:
  *   scale = max(max |y| / 448, 2^-100),  q = e4m3(y / scale), to nearest
+ * both NaN where a y of the row is.
  *   q      [B][T][d] bytes;  scale  [B][T]
  */
 ttt_status ttt_rmsnorm_q8_forward(int B, int T, int d, ttt_dtype dtype, float eps, const void* x,
@@ -470,7 +473,8 @@ ttt_status ttt_conv_backward(int B, int T, int C, int width, ttt_dtype dtype, in
  *   dt_t = softplus(dt[t] + dt_bias) (dt_softplus != 0) or dt[t] + dt_bias
  *   h_t[n] = exp(dt_t A[n]) h_{t-1}[n] + dt_t u_t B_t[n]
  *   y_t = (sum_n C_t[n] h_t[n] + D u_t) * silu(z_t)
- * 1 <= N <= 64; A is taken as it is (negative for a state that decays).
+ * 1 <= N <= 64; A is taken as it is (negative for a state that decays), minus
+ * infinity as the largest float.
  *   u, dt    [B][T][C], rows of ld_u, ld_dt elements
  *   dt_bias  [C] fp32 or NULL;  A  [C][N] fp32;  D  [C] fp32 or NULL
  *   Bm, Cm   [B][T][N], rows of ld_b, ld_c elements, shared by all channels

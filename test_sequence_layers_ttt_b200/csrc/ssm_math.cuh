@@ -37,7 +37,8 @@ __device__ __forceinline__ float decay(float x) {
 }
 
 // softplus(x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1]: log(1 + e) = 2 atanh(s), s = e / (2 + e) in
-// (0, 1/3], by an even polynomial that fits 2 atanh(s) / s to 8e-9; right to a few 1e-7 of the result at any x.
+// (0, 1/3], by an even polynomial that fits 2 atanh(s) / s to 8e-9; right to a few 1e-7 of the result for x > -5.  Below,
+// where the result is e^x, the rounding of x log2(e) counts about |x| 2^-24 of it (2e-6 at -40); below -87 it is 0.
 __device__ __forceinline__ float softplus(float x) {
     const float e = ex2(-kLog2e * fabsf(x));
     const float s = e * rcp(2.f + e), w = s * s;

@@ -17,7 +17,8 @@
 // Measured: 2 x 32768 rows of 2048, bf16 with a residual and an 8-bit output, 165 us, 5.7 TB/s, 0.87 of the copy
 // bandwidth; gradient of 32768 rows of 2048 in bf16 95 us, 0.86 of it; of 3 x 2731 rows of 2047 in fp32, rows that start
 // inside a vector, 68 us, 4.0 TB/s: three blocks an SM, all that its registers hold, leave the memory waiting in the
-// reductions.  4096 rows of 9001 in fp32 97 us forward (0.92) and 164 backward (0.55, one block an SM).
+// reductions.  4096 rows of 9001 in fp32 97 us forward (0.92) and 164 backward (0.55, one block an SM).  Two blocks of 512
+// threads an SM leave the 16-bit forward 64 registers a thread, and its main variant spills 32 to 56 bytes.
 //
 // Where d is no multiple of a vector (kShift), rows start inside one: a group counts its vectors from the
 // 16-byte boundary before its row, and the two at the ends go element by element.  The stride is a multiple of
@@ -241,7 +242,8 @@ __global__ void __launch_bounds__(512) ttt_rmsnorm_backward_kernel(const NormBwd
     const T* ip = p.dh_in ? static_cast<const T*>(p.dh_in) + (size_t)group * p.d : nullptr;
     const size_t stride = (size_t)groups * p.d;
     // Rows past 8192 leave no registers for the weight, which waits in shared memory (a thread's own part, 16 bytes
-    // side by side with its neighbours'), nor for h and dy in fp32 beside their 16 bits.
+    // side by side with its neighbours'), nor for h and dy in fp32 beside their 16 bits.  The widest variants spill all the
+    // same, up to 744 bytes a thread in fp32 and 512 in bf16.
     constexpr bool kWide = kNV * V > 16;
     extern __shared__ ulonglong2 wide[];
     const auto w_place = [&](int i, int k) -> ulonglong2& { return wide[(i * P / 2 + k) * blockDim.x + threadIdx.x]; };

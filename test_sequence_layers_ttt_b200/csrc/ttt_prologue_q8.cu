@@ -16,8 +16,10 @@
 // about a second without progress the kernel records an error word and stops waiting (outputs undefined;
 // TTT_ERR_TIMEOUT with TTT_CHECK=1).
 //
-// Measured (2 x 32768 tokens, d_model 2048, 32 heads): 0.70 ms, 2.4 PFLOP/s; without the epilogue's work 0.52 ms, with
-// all of it but the stores 0.58 ms.  The tensor pipe is busy for 67 % of the clocks.  Eight epilogue warps instead
+// Measured (2 x 32768 tokens, d_model 2048, 32 heads): 0.69 to 0.72 ms, 2.4 PFLOP/s, and 0.81 to 0.83 ms in a long run
+// of calls, when the power cap lowers the clock; without the epilogue's work 0.52 ms, with all of it but the stores
+// 0.58 ms.  One token of 64 streams: 14.6 us, 25 tiles on as many SMs.  The tensor pipe is busy for 67 % of the clocks,
+// and each CTA takes 48 KB of operands a K step through the L2, 10 GB in all.  Eight epilogue warps instead
 // of four, TMA stores and angles in fixed point took it there from 1.04 ms; a tile of 256 tokens in one CTA gave nothing.
 #include <cstdlib>
 

@@ -19,9 +19,10 @@
 // Sums over tokens are of chunks' sums in fp32, added in 64 bits.  What is left of dA's error (4e-7 to 9e-7 of its
 // norm over thousands of tokens) is the decays' rounding to fp32, which alone gives 4e-7 to 7e-7.
 //
-// Measured (8 x 2048 x 1536, 16 states, bf16): 1.00 ms, the second pass 0.79 and the first 0.21, of which HBM would take
-// 0.05 and the special functions 0.17.  The second pass issues in 56 % of the clocks and keeps the shared
-// memory pipe 60 % busy, most of it the shuffles and the states' way through shared memory.
+// Measured (8 x 2048 x 1536, 16 states): 1.02 ms in bf16, the second pass 0.80 and the first 0.22, and 1.01 in fp32.  The
+// special functions would take 0.17 of it, HBM 0.05 for the inputs and outputs and 0.06 for the chunks' states and the
+// blocks' parts of dB and dC, 100 MB each, written and read.  The second pass issues in 56 % of the clocks and keeps the
+// shared memory pipe 60 % busy, most of it the shuffles and the states' way through shared memory.
 #include "ssm_params.cuh"
 
 #include <algorithm>

@@ -7,9 +7,10 @@
 // pairs), and finish the last tile: the sum over the warps, D, the gate, the store.  One barrier a tile.
 //
 // Per token and 32 channels of 16 states an SM has 20 special-function results a channel (40 clocks), and on
-// each of its four schedulers 29 instructions of the recursion (34 clocks of the fp32 pipe) and about 12 of
-// the helpers.  Measured: 87 clocks (1.3B width, 32k tokens, bf16), 75 of them the recursion alone, which
-// waits on its own results: two channels a thread would hide that but leave half of the SMs idle.
+// each of its four schedulers 29 instructions of the recursion (34 clocks of the fp32 pipe); by the rate of issue the
+// helpers have some 25.  Measured: 1.41 ms, 89 clocks a token (1.3B width, 32k tokens, bf16; fp32 95), in 63 % of
+// which a scheduler issues; the recursion alone took 75, as it waits on its own results: two channels a thread would
+// hide that but leave half of the SMs idle.
 #include "ssm_params.cuh"
 
 #include <type_traits>
