@@ -10,8 +10,8 @@
 // nearest, is left.  Beyond it the unit's result stands: its error counts at most 16 times there.
 // The cost is three or four of the pipe's fused multiply-adds a state beside one special-function result
 // (16 a clock an SM), which stays the bound.  With the cubic for all states the scan of many channels took 1456 us
-// against 1414 (1.3B width, 32k tokens), so there a warp asks once whether any of its states grows; elsewhere it is used
-// for all (gradient of 8 x 2048 x 1536: 1.02 ms against 1.00).
+// against 1414 (1.3B width, 32k tokens), so there, and in the gradient's first pass, a warp asks once whether any of its
+// states grows; elsewhere it is used for all (gradient of 8 x 2048 x 1536: 1.02 ms against 1.00).
 #pragma once
 
 #include "vec_io.cuh"
